@@ -306,6 +306,93 @@ PA_API int pa_decode_noalloc(void* out, pa_dtype out_dtype, const void* q, const
                       int partition_size, pa_dtype dtype, int32_t* dev_err, pa_stream stream);
 
 /*
+ * pa_decode_weights -- pa_decode that also keeps, for each cached token, the
+ * running total of the attention weight it has received: what an eviction
+ * chooses by (pa_select_tokens).  With p_nj the softmax weight of query head n
+ * for token j,
+ *   weights_out[s][h][j] = weights_in[s][h][j] + sum over the query heads n of kv head h of p_nj
+ * for j < context_lens[s]; entries past the context are not written.
+ *
+ *   weights_out   fp32 [num_seqs][num_kv_heads][weights_stride], logical positions (not
+ *                 blocks: sequences that share blocks keep totals of their own)
+ *   weights_in    the same shape, or NULL: every total starts at zero.  May be
+ *                 weights_out (in place); must not overlap it otherwise.
+ *   weights_lens  int32 [num_seqs] (device), or NULL: entries of weights_in at positions
+ *                 >= weights_lens[s] count as zero.  Pass the lengths before the step
+ *                 where weights_in may hold anything behind them.
+ *   weights_stride  at least the context bound (max_context_len, or
+ *                 max_blocks_per_seq * block_size)
+ *   workspace     pa_decode_weights_workspace_bytes(), same arguments and rules as
+ *                 pa_decode's; it also holds one fp32 logit per query head and token of
+ *                 the bound, so bound the context (max_context_len) to what is in use.
+ * The rest, the arithmetic of `out` and the errors as for pa_decode, of which it
+ * is a variant that serves every sequence by itself (shared blocks are read once
+ * per sequence).  At most 256 query heads per kv head.  Totals are sums in fp32,
+ * heads in order.  A token in a block whose id is flagged receives weight zero.
+ */
+PA_API size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int head_dim,
+                                                int max_context_len, int partition_size);
+PA_API int pa_decode_weights(void* out, pa_dtype out_dtype, float* weights_out, const float* weights_in,
+                             const int32_t* weights_lens, int weights_stride, const void* q,
+                             const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                             const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                             int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                             int max_context_len, float scale, int partition_size, void* workspace,
+                             size_t workspace_bytes, pa_dtype dtype, int32_t* dev_err, pa_stream stream);
+
+/*
+ * pa_select_tokens -- the positions of each sequence and kv head that stay in
+ * the cache: the last min(recent, budget) ones and, of the others, the
+ * budget - recent with the largest totals (ties: the lowest positions; NaN
+ * counts as -infinity, -0 as 0).  A context within its budget stays whole.
+ *
+ *   keep          int32 [num_seqs][num_kv_heads][keep_stride]: the positions, ascending;
+ *                 entries past keep_lens[s] are not written
+ *   keep_lens     int32 [num_seqs]: min(context_lens[s], budgets[s]), the same for all heads
+ *   weights       fp32 [num_seqs][num_kv_heads][weights_stride] (pa_decode_weights)
+ *   context_lens  int32 [num_seqs], clamped to [0, weights_stride] and flagged PA_DEVERR_CONTEXT
+ *   budgets       int32 [num_seqs], clamped to [0, keep_stride] and flagged PA_DEVERR_CONTEXT
+ * One launch, no workspace.
+ */
+PA_API int pa_select_tokens(int32_t* keep, int32_t* keep_lens, const float* weights,
+                            const int32_t* context_lens, const int32_t* budgets, int num_seqs,
+                            int num_kv_heads, int weights_stride, int keep_stride, int recent,
+                            int32_t* dev_err, pa_stream stream);
+
+/*
+ * pa_compact -- moves kept tokens to consecutive positions: for every sequence
+ * s, kv head h and j < keep_lens[s], the K and V of position keep[s][h][j]
+ * (through src_tables) go to position starts[s] + j (through dst_tables), and
+ * its total, when given, from weights_in to weights_out.  For an eviction keep
+ * is pa_select_tokens' and starts NULL; for a verified tree of drafted tokens
+ * keep names the accepted path's positions (keep_heads 1) and starts the first
+ * drafted position.  Nothing else changes.  The copies are bit-exact.
+ *
+ *   keep          int32 [num_seqs][keep_heads][keep_stride]; keep_heads is num_kv_heads, or
+ *                 1: the same positions for every kv head.  keep[j] >= starts[s] + j.
+ *   starts        int32 [num_seqs], or NULL: 0
+ *   keep_lens     int32 [num_seqs], within [0, keep_stride]
+ *   src_tables    int32 [num_seqs][src_max_blocks]
+ *   dst_tables    int32 [num_seqs][dst_max_blocks]: entry i of row s is either entry i of
+ *                 src_tables' row s (in place) or a block that no row of src_tables names
+ *                 (a shared block must be replaced that way), and no two rows name the
+ *                 same destination block.  May be src_tables.
+ *   weights_in, weights_out  fp32 [num_seqs][num_kv_heads][weights_stride], both or neither;
+ *                 the same buffer (in place) or disjoint.  Totals at positions >=
+ *                 weights_stride do not move.
+ * An entry that would move up or lies outside a table is skipped (PA_DEVERR_COPY),
+ * one whose blocks are outside the pool too (PA_DEVERR_BLOCK_ID); a bad length or
+ * a negative start is flagged PA_DEVERR_CONTEXT (the length clamped, the sequence
+ * left as it was).  One launch, no workspace.
+ */
+PA_API int pa_compact(void* k_cache, void* v_cache, float* weights_out, const float* weights_in,
+                      int weights_stride, const int32_t* src_tables, const int32_t* dst_tables,
+                      int src_max_blocks, int dst_max_blocks, const int32_t* keep, int keep_heads,
+                      int keep_stride, const int32_t* starts, const int32_t* keep_lens, int num_seqs,
+                      int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_dtype dtype,
+                      int32_t* dev_err, pa_stream stream);
+
+/*
  * Host block manager -- the bookkeeping that produces block tables, slot
  * mappings and copy-on-write pairs (host memory only; no CUDA call).  After
  * "Month 2 · PagedAttention" sections 02-04 and the "PagedAttention blog"
@@ -365,6 +452,29 @@ PA_API int pa_bm_append(pa_block_manager* manager, int64_t seq_id, const int32_t
 PA_API int pa_bm_append_batch(pa_block_manager* manager, int num_seqs, const int64_t* seq_ids,
                               const int32_t* counts, const int32_t* token_ids, int64_t* slots,
                               int64_t* copies, int max_copies, int* num_copies, int* num_cached_tokens);
+/*
+ * pa_bm_compact -- the bookkeeping of one pa_compact call: sequence seq_ids[k]
+ * keeps num_tokens[k] tokens, of which the first unchanged[k] are those it had;
+ * the positions from there on receive kept tokens that stood behind them.
+ *  - Blocks past the new length are dropped (counts lowered, last block first).
+ *  - A block that receives tokens and is shared is replaced by a fresh one in the
+ *    sequence's table (its other sharers keep the old one).  Where tokens before
+ *    unchanged[k] stay in it, copies[2 * num_seqs] receives the (src, dst) block copy
+ *    to run before pa_compact, *num_copies the number of those.
+ *  - token_ids (prefix caching only, else ignored) are the ids of the tokens from
+ *    unchanged[k] on, all sequences' in a row; NULL: unknown (an eviction by kv head),
+ *    and blocks that a sequence fills from there on are neither cached nor looked up.
+ *    Blocks that receive tokens leave the prefix cache; those that known ids fill enter it.
+ * Read the tables before the call (src_tables) and after it (dst_tables); they fit
+ * pa_compact's rule.  Dropped blocks may be handed out again by the next call: launch
+ * pa_compact before anything that writes them, on the same stream.
+ * PA_ERR_INVALID_ARG for an unknown or repeated id or lengths not in 0 <= unchanged <=
+ * num_tokens <= the sequence's; PA_ERR_WORKSPACE if the fresh blocks exceed the free
+ * ones.  Nothing changes then.
+ */
+PA_API int pa_bm_compact(pa_block_manager* manager, int num_seqs, const int64_t* seq_ids,
+                         const int64_t* unchanged, const int64_t* num_tokens, const int32_t* token_ids,
+                         int64_t* copies, int* num_copies);
 /* The sequence's block table (out may be NULL to query *num_blocks); PA_ERR_WORKSPACE if
  * it has more than max_blocks entries.  *num_tokens (nullable) gets its length. */
 PA_API int pa_bm_block_table(const pa_block_manager* manager, int64_t seq_id, int32_t* out,

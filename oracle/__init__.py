@@ -16,7 +16,8 @@ Sources (web pages on PagedAttention):
     attention that gathers K and V from non-contiguous addresses).
 
 Every function here is pinned by a ``-m "not gpu"`` test in
-``tests/test_oracle_pins.py``; none is "parity unpinned".
+``tests/test_oracle_pins.py`` or ``tests/test_cache_drop_cpu.py``; none is
+"parity unpinned".
 """
 
 from .paged_attention import (  # noqa: F401
@@ -26,4 +27,10 @@ from .paged_attention import (  # noqa: F401
     prefill_attention,
     reshape_and_cache,
     copy_blocks,
+)
+from .cache_drop import (  # noqa: F401
+    tree_attention,
+    attention_weights,
+    select_tokens,
+    compact,
 )

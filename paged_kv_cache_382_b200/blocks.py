@@ -129,6 +129,34 @@ class BlockManager:
             self.pool.incref(block)
         return Sequence(block_table=list(seq.block_table), num_tokens=seq.num_tokens)
 
+    def compact(self, seqs: List[Sequence], unchanged: List[int], num_tokens: List[int]) -> List[Tuple[int, int]]:
+        """Sequence ``seqs[k]`` keeps ``num_tokens[k]`` tokens: its first ``unchanged[k]`` ones, then
+        tokens moved down from behind.
+
+        Shared blocks that receive tokens are replaced by fresh ones, all of them before any block
+        past a new length is dropped.  Returns the (src, dst) block copies that must run before the
+        moves (for blocks that also hold unchanged tokens)."""
+        B = self.block_size
+        for seq, u, n in zip(seqs, unchanged, num_tokens):
+            if not 0 <= u <= n <= seq.num_tokens:
+                raise ValueError("0 <= unchanged <= num_tokens <= the sequence's tokens")
+        fresh = [(seq, u, i, seq.block_table[i]) for seq, u, n in zip(seqs, unchanged, num_tokens) if u < n
+                 for i in range(u // B, -(-n // B)) if self.pool.ref_cnt[seq.block_table[i]] > 1]
+        if len(fresh) > self.pool.num_free:
+            raise OutOfBlocks(f"a compaction needs {len(fresh)} fresh blocks")
+        copies: List[Tuple[int, int]] = []
+        for seq, u, i, old in fresh:
+            seq.block_table[i] = self.pool.allocate()
+            if i == u // B and u % B:
+                copies.append((old, seq.block_table[i]))
+        for _, _, _, old in fresh:
+            self.pool.decref(old)
+        for seq, n in zip(seqs, num_tokens):
+            while len(seq.block_table) > -(-n // B):
+                self.pool.decref(seq.block_table.pop())
+            seq.num_tokens = n
+        return copies
+
     def free(self, seq: Sequence) -> None:
         # last block first: under least-recently-freed reuse a shared prefix stays longest
         for block in reversed(seq.block_table):

@@ -217,10 +217,16 @@ struct LaneFrag {
 // O^T += V^T . P^T.  `st` is the stage's shared-memory address; bit r of `mask`
 // says whether token row r takes part (its V row must then hold finite values;
 // excluded rows' V must be zero).  qf: the lane's B fragments of its query
-// column (g), d = 16 ks + 2c (+ 8).
-template <int D, int RB>
+// column (g), d = 16 ks + 2c (+ 8).  `sink` receives the lane's masked logits
+// (log2 domain) of tokens g and g + 8, columns 2c and 2c + 1; NoSink drops them.
+struct NoSink {
+    __device__ __forceinline__ void operator()(float, float, float, float) const {}
+};
+
+template <int D, int RB, typename Sink = NoSink>
 __device__ __forceinline__ void attend_tile(StreamState<D>& S, uint32_t st, const uint32_t (&qf)[D / 16][2],
-                                            unsigned mask, float sl2, const LaneFrag<D, RB>& f, int g) {
+                                            unsigned mask, float sl2, const LaneFrag<D, RB>& f, int g,
+                                            const Sink& sink = Sink()) {
     using Geo = TileGeom<D, RB>;
     constexpr int KS = D / 16, NH = Geo::NH, HALF = Geo::HALF;
     // S^T (16 tokens x 8 columns) as two independent accumulation chains
@@ -242,6 +248,7 @@ __device__ __forceinline__ void attend_tile(StreamState<D>& S, uint32_t st, cons
         if (!((mask >> g) & 1u)) x0 = x1 = NEG_INF;
         if (!((mask >> (g + 8)) & 1u)) x2 = x3 = NEG_INF;
     }
+    sink(x0, x1, x2, x3);
     float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {

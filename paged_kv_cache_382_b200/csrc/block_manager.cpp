@@ -20,8 +20,10 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <new>
 #include <unordered_map>
+#include <unordered_set>
 #include <vector>
 
 #include "../../include/pa.h"
@@ -33,6 +35,10 @@ struct Sequence {
     int64_t num_tokens = 0;
     uint64_t last_full_hash = 0;          // hash of the last full block (chain seed)
     std::vector<int32_t> partial_tokens;  // tokens of the current partly filled block
+    // prefix caching only: what a compaction cuts back to
+    std::vector<uint64_t> hashes;         // chained hash of every full block
+    std::vector<int32_t> tokens;          // every token's id
+    bool keyed = true;                    // ids known: false from an eviction on (blocks no longer cached)
 };
 
 }  // namespace
@@ -165,6 +171,25 @@ extern "C" int pa_bm_free(pa_block_manager* m, int64_t seq_id) {
 
 namespace {
 
+// Prefix caching: token `id` now stands at the end of sq's block b; a block it
+// fills is cached.
+void note_token(pa_block_manager* m, Sequence& sq, int32_t b, int32_t id) {
+    const int B = m->block_size;
+    sq.tokens.push_back(id);
+    sq.partial_tokens.push_back(id);
+    if (static_cast<int>(sq.partial_tokens.size()) < B) return;
+    const uint64_t h = chain_hash(sq.last_full_hash, sq.partial_tokens.data(), B);
+    sq.last_full_hash = h;
+    sq.hashes.push_back(h);
+    if (m->block_hash[b] == 0 && !m->cached.count(h)) {
+        m->cached.emplace(h, b);
+        m->block_hash[b] = h;
+        std::copy(sq.partial_tokens.begin(), sq.partial_tokens.end(),
+                  m->block_tokens.begin() + static_cast<size_t>(b) * B);
+    }
+    sq.partial_tokens.clear();
+}
+
 // Appends n tokens to sq; slots[n] gets their slots, copies (room for
 // max_copies pairs) the copy-on-write pairs, counted into *num_copies;
 // *cached (nullable) counts the tokens found in the prefix cache.
@@ -178,7 +203,7 @@ int append_tokens(pa_block_manager* m, Sequence& sq, const int32_t* token_ids, i
         const int off = static_cast<int>(pos % B);
         if (off == 0 && logical == static_cast<int64_t>(sq.table.size())) {
             // a new logical block: reuse a cached one if the next B tokens form a known block
-            if (m->prefix_cache && num_tokens - i >= B) {
+            if (m->prefix_cache && sq.keyed && num_tokens - i >= B) {
                 const uint64_t h = chain_hash(sq.last_full_hash, token_ids + i, B);
                 auto hit = m->cached.find(h);
                 if (hit != m->cached.end()) {
@@ -190,6 +215,8 @@ int append_tokens(pa_block_manager* m, Sequence& sq, const int32_t* token_ids, i
                         m->incref(b);
                         sq.table.push_back(b);
                         sq.last_full_hash = h;
+                        sq.hashes.push_back(h);
+                        sq.tokens.insert(sq.tokens.end(), token_ids + i, token_ids + i + B);
                         for (int k = 0; k < B; ++k) slots[i + k] = -1;   // already in the pool
                         sq.num_tokens += B;
                         i += B;
@@ -219,20 +246,7 @@ int append_tokens(pa_block_manager* m, Sequence& sq, const int32_t* token_ids, i
         }
         const int32_t b = sq.table[logical];
         slots[i] = static_cast<int64_t>(b) * B + off;
-        if (m->prefix_cache) {
-            sq.partial_tokens.push_back(token_ids[i]);
-            if (static_cast<int>(sq.partial_tokens.size()) == B) {   // block full: cache it
-                const uint64_t h = chain_hash(sq.last_full_hash, sq.partial_tokens.data(), B);
-                sq.last_full_hash = h;
-                if (m->block_hash[b] == 0 && !m->cached.count(h)) {
-                    m->cached.emplace(h, b);
-                    m->block_hash[b] = h;
-                    std::copy(sq.partial_tokens.begin(), sq.partial_tokens.end(),
-                              m->block_tokens.begin() + static_cast<size_t>(b) * B);
-                }
-                sq.partial_tokens.clear();
-            }
-        }
+        if (m->prefix_cache && sq.keyed) note_token(m, sq, b, token_ids[i]);
         ++sq.num_tokens;
         ++i;
     }
@@ -275,6 +289,93 @@ extern "C" int pa_bm_append_batch(pa_block_manager* m, int num_seqs, const int64
                                      counts[k], slots + at, copies, max_copies, num_copies, num_cached_tokens);
         if (rc != PA_OK) return rc;
         at += counts[k];
+    }
+    return PA_OK;
+}
+
+namespace {
+
+// Prefix caching after a compaction: sq's tokens from `unchanged` on are
+// ids[0 .. num_tokens - unchanged), or unknown (ids null).
+void rekey(pa_block_manager* m, Sequence& sq, int64_t unchanged, int64_t num_tokens, const int32_t* ids) {
+    const int64_t B = m->block_size;
+    if (ids == nullptr && unchanged < num_tokens) {
+        sq.keyed = false;
+        sq.hashes.clear();
+        sq.tokens.clear();
+        sq.partial_tokens.clear();
+        return;
+    }
+    sq.hashes.resize(static_cast<size_t>(unchanged / B));
+    sq.tokens.resize(static_cast<size_t>(unchanged));
+    sq.last_full_hash = sq.hashes.empty() ? 0 : sq.hashes.back();
+    sq.partial_tokens.assign(sq.tokens.begin() + static_cast<std::ptrdiff_t>(unchanged / B * B), sq.tokens.end());
+    for (int64_t p = unchanged; p < num_tokens; ++p)
+        note_token(m, sq, sq.table[static_cast<size_t>(p / B)], ids[p - unchanged]);
+}
+
+}  // namespace
+
+extern "C" int pa_bm_compact(pa_block_manager* m, int num_seqs, const int64_t* seq_ids, const int64_t* unchanged,
+                             const int64_t* num_tokens, const int32_t* token_ids, int64_t* copies, int* num_copies) {
+    if (!m || num_seqs < 0 || !num_copies) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!seq_ids || !unchanged || !num_tokens || !copies)) return PA_ERR_INVALID_ARG;
+    const int64_t B = m->block_size;
+    std::vector<Sequence*> sqs(static_cast<size_t>(num_seqs));
+    std::unordered_set<int64_t> named;
+    // logical blocks [first, kept) of a sequence receive tokens (none when it is only cut)
+    auto kept = [&](int k) { return (num_tokens[k] + B - 1) / B; };
+    auto first = [&](int k) { return unchanged[k] < num_tokens[k] ? unchanged[k] / B : kept(k); };
+    struct Fresh {
+        Sequence* sq;
+        int64_t at;
+        int32_t old;
+    };
+    std::vector<Fresh> fresh;   // shared blocks to replace, by the counts before the call
+    for (int k = 0; k < num_seqs; ++k) {   // everything checked before anything changes
+        auto it = m->seqs.find(seq_ids[k]);
+        if (it == m->seqs.end() || !named.insert(seq_ids[k]).second || unchanged[k] < 0 ||
+            num_tokens[k] < unchanged[k] || num_tokens[k] > it->second.num_tokens)
+            return PA_ERR_INVALID_ARG;
+        sqs[k] = &it->second;
+        for (int64_t i = first(k); i < kept(k); ++i) {
+            const int32_t old = sqs[k]->table[i];
+            if (m->ref_cnt[old] > 1) fresh.push_back({sqs[k], i, old});
+        }
+    }
+    *num_copies = 0;
+    if (static_cast<int64_t>(fresh.size()) > m->num_free) return PA_ERR_WORKSPACE;
+    // every fresh block is taken before any block is dropped: a dropped one may
+    // still be a source of the moves
+    size_t f = 0;
+    for (int k = 0; k < num_seqs; ++k) {
+        for (int64_t i = first(k); i < kept(k); ++i) {
+            if (f < fresh.size() && fresh[f].sq == sqs[k] && fresh[f].at == i) {
+                sqs[k]->table[i] = m->allocate();
+                if (i == first(k) && unchanged[k] % B != 0) {
+                    copies[2 * *num_copies] = fresh[f].old;
+                    copies[2 * *num_copies + 1] = sqs[k]->table[i];
+                    ++*num_copies;
+                }
+                ++f;
+            } else {
+                m->evict(sqs[k]->table[i]);   // its cached contents are overwritten
+            }
+        }
+    }
+    for (const Fresh& x : fresh) m->decref(x.old);
+    const int32_t* ids = token_ids;
+    for (int k = 0; k < num_seqs; ++k) {
+        Sequence& sq = *sqs[k];
+        while (static_cast<int64_t>(sq.table.size()) > kept(k)) {
+            m->decref(sq.table.back());
+            sq.table.pop_back();
+        }
+        // a cut inside a full block: its later slots will be written again
+        if (num_tokens[k] % B != 0 && m->ref_cnt[sq.table.back()] == 1) m->evict(sq.table.back());
+        sq.num_tokens = num_tokens[k];
+        if (m->prefix_cache && sq.keyed) rekey(m, sq, unchanged[k], num_tokens[k], ids);
+        if (ids != nullptr) ids += num_tokens[k] - unchanged[k];
     }
     return PA_OK;
 }

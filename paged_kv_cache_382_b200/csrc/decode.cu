@@ -88,6 +88,12 @@ struct DecodeArgs {
     int out_f32;         // 1: out is fp32, 0: out is bf16
     int pack;            // sequences a packed item may serve (8 * ATTEND_WARPS / group; 1 = no packing)
     const int32_t* row_seq;   // prefill: the sequence (block-table row) of each query row; null = identity
+    // pa_decode_weights only (else null / 0)
+    float* ws_x;              // [num_seqs][num_kv_heads][cap][group]  logits of every token (log2 domain)
+    const float* w_in;        // [num_seqs][num_kv_heads][w_stride] totals before the step; null: all zero
+    float* w_out;             // the same shape; may be w_in
+    const int32_t* w_lens;    // [num_seqs] entries of w_in that count; null: all of the context
+    int w_stride;
 };
 
 // Block-table row of query row s: its own row for decode; for prefill, the row
@@ -484,7 +490,8 @@ __device__ __forceinline__ int unit_rows(const DecodeArgs& a, int hg, int count)
 }
 
 // row_info[n] = (sequence, head, partitions of that sequence) of query row n.
-template <int W, int D>
+// LOGITS: the (max, sum) of a single partition is kept too (pa_decode_weights).
+template <int W, int D, bool LOGITS>
 __device__ __forceinline__ void combine_store(const DecodeArgs& a, const float* mm, const float* ml,
                                               const float* mo, const int3* row_info, int p, int nrows) {
     for (int idx = threadIdx.x; idx < nrows * D; idx += W * 32) {
@@ -509,6 +516,7 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, const float* 
                 static_cast<float*>(a.out)[row * D + d] = v;
             else
                 static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(v);
+            if (LOGITS && d == 0) a.ws_ml[row * a.max_parts] = make_float2(M, L);
         } else {
             const size_t slot = row * a.max_parts + p;
             a.ws_acc[slot * D + d] = O;
@@ -516,6 +524,33 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, const float* 
         }
     }
 }
+
+// Where a unit's logits go: ws_x row of its first token, this head group's columns.
+__device__ __forceinline__ float* logits_row(const DecodeArgs& a, int s, int kvh, int hg, int t0) {
+    return a.ws_x + ((static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.cap + t0) * a.group + hg * 8;
+}
+
+// Stores a lane's logits of one 16-token tile: tokens row and row + 8 of the
+// tile, columns col and col + 1, those below the tile's tokens and the head
+// group's columns.  An even group keeps the pair aligned: one 8-byte store.
+struct LogitSink {
+    float* x;   // the tile's first token, the lane's first column
+    int group, row, rows, cols;   // rows / cols: tokens of the tile, columns from the lane's first on
+    __device__ __forceinline__ void put(int r, float a, float b) const {
+        if (r >= rows) return;
+        float* at = x + static_cast<size_t>(r) * group;
+        if (cols >= 2 && (group & 1) == 0) {
+            *reinterpret_cast<float2*>(at) = make_float2(a, b);
+        } else {
+            if (cols >= 1) at[0] = a;
+            if (cols >= 2) at[1] = b;
+        }
+    }
+    __device__ __forceinline__ void operator()(float x0, float x1, float x2, float x3) const {
+        put(row, x0, x1);
+        put(row + 8, x2, x3);
+    }
+};
 
 // ---------------------------------------------------------------------------
 // 2a. attend, bf16 (tile arithmetic, stream states and merges: attend_bf16.cuh)
@@ -546,7 +581,9 @@ __device__ __forceinline__ void store_final(const StreamState<D>& S, float* fin_
     }
 }
 
-template <int D, int RB, int W, int NS>
+// LOGITS (pa_decode_weights): every logit is also written to ws_x, and the
+// (max, sum) of single partitions to ws_ml; the plan packs nothing then.
+template <int D, int RB, int W, int NS, bool LOGITS>
 __global__ void __launch_bounds__(W * 32, PA_ATTEND_MIN_CTAS)
 attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const DecodeArgs a) {
@@ -726,7 +763,7 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         S.reset();
         bool failed = false;
 
-        if (ncg == 1) {
+        if (LOGITS || ncg == 1) {
             // ---- one column group: warp w runs stream w through its own ring
             const int my_tiles = warp < ntiles ? (ntiles - warp + W - 1) / W : 0;   // = qn + (warp < rem)
             // Issue the bulk copies of this warp's j-th tile into the next ring stage.
@@ -793,7 +830,13 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                attend_tile<D, RB>(S, st, qf, mask, sl2, frag, g);
+                if constexpr (LOGITS) {
+                    const LogitSink sink{logits_row(a, s, kvh, hg, t0 + r0) + 2 * c, a.group, g, ntok - r0,
+                                         nrows - 2 * c};
+                    attend_tile<D, RB>(S, st, qf, mask, sl2, frag, g, sink);
+                } else {
+                    attend_tile<D, RB>(S, st, qf, mask, sl2, frag, g);
+                }
                 __syncwarp();
                 if (j + NS < my_tiles) issue(j + NS);
             }
@@ -932,7 +975,7 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             break;
         }
         const float* slots = reinterpret_cast<const float*>(stages);
-        if (split_slot >= 0) {
+        if (!LOGITS && split_slot >= 0) {
             // every stream's state is in the workspace once all W CTAs have counted
             // themselves; the last one merges them in stream order (the merge of
             // merge_into_slot / merge_slot_first) and writes the unit's outputs
@@ -954,7 +997,7 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     merge_global_second<D>(S, st0 + static_cast<size_t>(sidx) * W * (State::FLOATS * 32), lane);
             }
         }
-        if (ncg == 1) {
+        if (LOGITS || ncg == 1) {
             // the W stream states wait in slots; every thread merges some of the
             // unit's (column, element) pairs, streams in order (the arithmetic of
             // merge_into_slot / merge_slot_first, element by element)
@@ -969,7 +1012,7 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const int3 ri = s_rows[n];
             float O[4];
             float2 ml;
-            if (ncg == 1) {
+            if (LOGITS || ncg == 1) {
                 // lane (g, c) holds columns 2c, 2c+1 and elements 16i + g (+8); the
                 // four elements sit in lanes 4g + c of one slot element each
                 const int e = (n & 1) + 2 * ((d0 >> 3) & 1), i16 = d0 >> 4;
@@ -1007,6 +1050,7 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 else
                     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d0) =
                         make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                if (LOGITS && d0 == 0) a.ws_ml[row * a.max_parts] = ml;
             } else {
                 const size_t slot = row * a.max_parts + p;
                 *reinterpret_cast<float4*>(a.ws_acc + slot * D + d0) = make_float4(O[0], O[1], O[2], O[3]);
@@ -1021,7 +1065,7 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 // 2b. attend, fp32: CUDA cores, one warp per token, lanes split the head dim
 // ---------------------------------------------------------------------------
 
-template <int D>
+template <int D, bool LOGITS>
 __global__ void __launch_bounds__(128, 2) attend_f32_kernel(const DecodeArgs a) {
     constexpr int W = 4, J = D / 32;
     __shared__ float mm[W * 8], ml[W * 8];
@@ -1065,6 +1109,7 @@ __global__ void __launch_bounds__(128, 2) attend_f32_kernel(const DecodeArgs a) 
             const int phys = table_row(a, s)[t / B];
             if (phys < 0 || phys >= a.num_blocks) {
                 if (lane == 0) flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
+                if (LOGITS && lane < gsub) logits_row(a, s, kvh, hg, t)[lane] = NEG_INF;   // takes no part
                 continue;
             }
             const size_t rowi = ((static_cast<size_t>(phys) * a.num_kv_heads + kvh) * B + t % B) * D;
@@ -1083,6 +1128,7 @@ __global__ void __launch_bounds__(128, 2) attend_f32_kernel(const DecodeArgs a) 
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(FULL_MASK, dot, off);
                 const float x = dot * a.scale_log2;
+                if (LOGITS && lane == 0) logits_row(a, s, kvh, hg, t)[n] = x;
                 const float mn = fmaxf(m[n], x);
                 const float al = exp2_approx(m[n] - mn);
                 const float pw = exp2_approx(x - mn);
@@ -1106,7 +1152,7 @@ __global__ void __launch_bounds__(128, 2) attend_f32_kernel(const DecodeArgs a) 
 #pragma unroll
             for (int j = 0; j < J; ++j) mo[(warp * 8 + n) * D + lane + 32 * j] = acc[n][j];
         __syncthreads();
-        combine_store<W, D>(a, mm, ml, mo, s_rows, p, gsub);
+        combine_store<W, D, LOGITS>(a, mm, ml, mo, s_rows, p, gsub);
     }
 }
 
@@ -1284,6 +1330,69 @@ __global__ void __launch_bounds__(REDUCE_PARTS_THREADS, 4) reduce_parts_kernel(c
 }
 
 // ---------------------------------------------------------------------------
+// weights: each cached token's attention weight, summed over the query heads
+// of its kv head and added to its running total (pa_decode_weights):
+//   w_out[s][h][j] = w_in[s][h][j] + sum_n 2^(x_jn - M_n) / L_n,
+// x from ws_x, (M_n, L_n) the merged (max, sum) of head n's partitions.
+// A weight needs the whole context's sum, which no partition knows while it
+// runs: hence the logits' round trip, 8 * group bytes per token and kv head
+// next to the 2 * d * e of its K and V, mostly through L2.
+// ---------------------------------------------------------------------------
+
+constexpr int WEIGHTS_THREADS = 256;
+constexpr int WEIGHTS_PER_THREAD = 2;
+constexpr int WEIGHTS_TOKENS = WEIGHTS_THREADS * WEIGHTS_PER_THREAD;   // tokens per CTA
+constexpr int WEIGHTS_MAX_GROUP = 256;   // query heads per kv head (their coefficients sit in shared memory)
+
+__global__ void __launch_bounds__(WEIGHTS_THREADS) weights_kernel(const DecodeArgs a, int chunks) {
+    __shared__ float2 s_ml[WEIGHTS_MAX_GROUP];   // (max, 1 / sum) of each query head
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = blockIdx.x / chunks;         // s * num_kv_heads + kvh
+    const int t0 = (blockIdx.x - row * chunks) * WEIGHTS_TOKENS;
+    const int s = row / a.num_kv_heads, kvh = row - s * a.num_kv_heads, G = a.group;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int ctx = clamp_context(a.context_lens[s], a.cap);
+    if (t0 >= ctx) return;
+    const int nparts = (ctx + a.partition_size - 1) / a.partition_size;
+    for (int n = warp; n < G; n += WEIGHTS_THREADS / 32) {
+        const float2* ml = a.ws_ml + (static_cast<size_t>(s) * a.num_heads + kvh * G + n) * a.max_parts;
+        float M = NEG_INF, L = 0.f;
+        for (int p = lane; p < nparts; p += 32) M = fmaxf(M, ml[p].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, off));
+        if (M != NEG_INF)
+            for (int p = lane; p < nparts; p += 32) L = fmaf(exp2_approx(ml[p].x - M), ml[p].y, L);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(FULL_MASK, L, off);
+        if (lane == 0) s_ml[n] = make_float2(M == NEG_INF ? 0.f : M, L > 0.f ? 1.f / L : 0.f);
+    }
+    __syncthreads();
+    const int counted = a.w_lens != nullptr ? a.w_lens[s] : ctx;
+    const size_t wrow = static_cast<size_t>(row) * a.w_stride;
+#pragma unroll
+    for (int k = 0; k < WEIGHTS_PER_THREAD; ++k) {
+        const int t = t0 + k * WEIGHTS_THREADS + tid;
+        if (t >= ctx) break;
+        const float* x = a.ws_x + (static_cast<size_t>(row) * a.cap + t) * G;
+        float w = 0.f;
+        if ((G & 3) == 0) {
+            for (int n = 0; n < G; n += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(x + n);
+                w = fmaf(exp2_approx(v.x - s_ml[n].x), s_ml[n].y, w);
+                w = fmaf(exp2_approx(v.y - s_ml[n + 1].x), s_ml[n + 1].y, w);
+                w = fmaf(exp2_approx(v.z - s_ml[n + 2].x), s_ml[n + 2].y, w);
+                w = fmaf(exp2_approx(v.w - s_ml[n + 3].x), s_ml[n + 3].y, w);
+            }
+        } else {
+            for (int n = 0; n < G; ++n) w = fmaf(exp2_approx(x[n] - s_ml[n].x), s_ml[n].y, w);
+        }
+        const float before = (a.w_in != nullptr && t < counted) ? a.w_in[wrow + t] : 0.f;
+        a.w_out[wrow + t] = before + w;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // prefill: each new token becomes one query row of the decode machinery, with
 // its sequence's block table and a context that ends at its own position
 // (the causal mask), so consecutive new tokens of a sequence share every whole
@@ -1320,7 +1429,7 @@ prefill_rows_kernel(const int32_t* __restrict__ context_lens, const int32_t* __r
 inline size_t round_up(size_t v, size_t m) { return (v + m - 1) / m * m; }
 
 struct WsLayout {
-    size_t items, ml, acc, split, split_cnt, total;
+    size_t items, ml, acc, split, split_cnt, x, total;
     int split_cap;
 };
 
@@ -1331,7 +1440,8 @@ inline int split_cap_for(int S, int Hq, int max_parts) {
     return static_cast<int>(bound < SPLIT_CAP_MAX ? bound : SPLIT_CAP_MAX);
 }
 
-inline WsLayout ws_layout(int S, int Hq, int D, int max_parts) {
+// logits_cap: the context bound when the logits are kept (pa_decode_weights), else 0.
+inline WsLayout ws_layout(int S, int Hq, int D, int max_parts, int logits_cap = 0) {
     WsLayout L;
     L.split_cap = split_cap_for(S, Hq, max_parts);
     size_t off = 256;   // header: the work-item count (0) and the attend kernel's unit ticket (8)
@@ -1339,19 +1449,22 @@ inline WsLayout ws_layout(int S, int Hq, int D, int max_parts) {
     // every (sequence, partition) item, plus W - 1 more for each split one
     off += round_up((static_cast<size_t>(S) * max_parts + static_cast<size_t>(ATTEND_STREAMS - 1) * L.split_cap) *
                         sizeof(int4), 256);
-    if (max_parts > 1) {
+    L.ml = L.acc = 0;
+    if (max_parts > 1 || logits_cap > 0) {
         L.ml = off;
         off += round_up(static_cast<size_t>(S) * Hq * max_parts * sizeof(float2), 256);
+    }
+    if (max_parts > 1) {
         L.acc = off;
         off += round_up(static_cast<size_t>(S) * Hq * max_parts * D * sizeof(float), 256);
-    } else {
-        L.ml = L.acc = 0;
     }
     L.split = off;
     off += round_up(static_cast<size_t>(L.split_cap) * ATTEND_STREAMS * ATTEND_WARPS * (4 * (D / 16) + 4) * 32 *
                         sizeof(float), 256);
     L.split_cnt = off;
     off += round_up(static_cast<size_t>(L.split_cap) * sizeof(int), 256);
+    L.x = off;
+    off += round_up(static_cast<size_t>(S) * Hq * logits_cap * sizeof(float), 256);
     L.total = off;
     return L;
 }
@@ -1361,7 +1474,7 @@ inline int parts_for(int cap, int P) {
     return n < 1 ? 1 : n;
 }
 
-template <int D, int RB>
+template <int D, int RB, bool LOGITS>
 int launch_attend_bf16(const DecodeArgs& a, cudaStream_t st, long long unit_bound) {
     using Geo = TileGeom<D, RB>;
     constexpr int W = ATTEND_WARPS, NS = ATTEND_STAGES;
@@ -1375,7 +1488,7 @@ int launch_attend_bf16(const DecodeArgs& a, cudaStream_t st, long long unit_boun
     // counters per stage, the table slice
     const int smem = 1024 + W * NS * Geo::STAGE + 2 * W * NS * 8 + 2 * W * NS * 4 + tbl_entries * 4 +
                      (a.partition_size / 16) * 2;
-    auto kern = attend_bf16_kernel<D, RB, W, NS>;
+    auto kern = attend_bf16_kernel<D, RB, W, NS, LOGITS>;
     const int per_sm = prepare_kernel(slot, reinterpret_cast<const void*>(kern), W * 32, smem);
     int dev = 0;
     const int sms = current_sm_count(&dev);
@@ -1386,10 +1499,10 @@ int launch_attend_bf16(const DecodeArgs& a, cudaStream_t st, long long unit_boun
     return launch_status(launch_pdl(kern, dim3(grid), dim3(W * 32), smem, st, tk, tv, a));
 }
 
-template <int D>
+template <int D, bool LOGITS>
 int launch_attend_f32(const DecodeArgs& a, cudaStream_t st, long long unit_bound) {
     static KernelSlot slot;
-    auto kern = attend_f32_kernel<D>;
+    auto kern = attend_f32_kernel<D, LOGITS>;
     const int per_sm = prepare_kernel(slot, reinterpret_cast<const void*>(kern), 128, 0);
     const int sms = current_sm_count();
     if (per_sm <= 0 || sms <= 0) return PA_ERR_CUDA;
@@ -1398,6 +1511,30 @@ int launch_attend_f32(const DecodeArgs& a, cudaStream_t st, long long unit_bound
     if (grid <= 0) return PA_OK;
     return launch_status(launch_pdl(kern, dim3(grid), dim3(128), 0, st, a));
 }
+
+template <bool LOGITS>
+int launch_attend(const DecodeArgs& a, pa_dtype dtype, cudaStream_t st) {
+    const long long unit_bound = static_cast<long long>(a.num_seqs) * a.max_parts * a.num_kv_heads * a.head_groups;
+    if (dtype != PA_BF16)
+        return a.head_dim == 128 ? launch_attend_f32<128, LOGITS>(a, st, unit_bound)
+                                 : launch_attend_f32<64, LOGITS>(a, st, unit_bound);
+    const int rb = a.block_size < 16 ? a.block_size : 16;
+    if (a.head_dim == 128)
+        return rb == 16 ? launch_attend_bf16<128, 16, LOGITS>(a, st, unit_bound)
+               : rb == 8 ? launch_attend_bf16<128, 8, LOGITS>(a, st, unit_bound)
+                         : launch_attend_bf16<128, 4, LOGITS>(a, st, unit_bound);
+    return rb == 16 ? launch_attend_bf16<64, 16, LOGITS>(a, st, unit_bound)
+           : rb == 8 ? launch_attend_bf16<64, 8, LOGITS>(a, st, unit_bound)
+                     : launch_attend_bf16<64, 4, LOGITS>(a, st, unit_bound);
+}
+
+// The totals pa_decode_weights keeps.
+struct WeightArgs {
+    const float* in;
+    float* out;
+    const int32_t* lens;
+    int stride;
+};
 
 }  // namespace pa
 
@@ -1450,7 +1587,8 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
                        int num_blocks, int max_blocks_per_seq, int max_context_len, float scale,
                        int partition_size, void* workspace, size_t workspace_bytes, pa_dtype dtype,
                        int32_t* dev_err, pa_stream stream, int phases, const int32_t* row_seq,
-                       Prep prep, const ScatterArgs* scatter = nullptr, int num_new_tokens = 0) {
+                       Prep prep, const ScatterArgs* scatter = nullptr, int num_new_tokens = 0,
+                       const WeightArgs* weights = nullptr) {
     // ---- host-side validation: nothing is launched unless everything is sane
     const int shape_rc = check_shapes(out_dtype, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
                                       num_blocks, max_blocks_per_seq, max_context_len, scale, partition_size,
@@ -1462,7 +1600,15 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
     const long long cap = context_cap(max_blocks_per_seq, block_size, max_context_len);
     const int max_parts = parts_for(static_cast<int>(cap), partition_size);
     if (static_cast<long long>(num_seqs) * max_parts > (INT_MAX >> ITEM_LOW_BITS)) return PA_ERR_UNSUPPORTED;
-    const WsLayout L = ws_layout(num_seqs, num_heads, head_dim, max_parts);
+    if (weights != nullptr) {
+        if (num_heads / num_kv_heads > WEIGHTS_MAX_GROUP ||
+            static_cast<long long>(num_seqs) * num_kv_heads * (cap / WEIGHTS_TOKENS + 1) > INT_MAX)
+            return PA_ERR_UNSUPPORTED;
+        if (!weights->out || !aligned_to(weights->out, 4) || (weights->in && !aligned_to(weights->in, 4)) ||
+            (weights->lens && !aligned_to(weights->lens, 4)) || weights->stride < cap)
+            return PA_ERR_INVALID_ARG;
+    }
+    const WsLayout L = ws_layout(num_seqs, num_heads, head_dim, max_parts, weights ? static_cast<int>(cap) : 0);
     if (!workspace || !aligned_to(workspace, 256)) return PA_ERR_INVALID_ARG;
     if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
     if (!context_lens || !aligned_to(context_lens, 4)) return PA_ERR_INVALID_ARG;
@@ -1491,7 +1637,7 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
     a.ws_split = reinterpret_cast<float*>(ws + L.split);
     a.ws_split_cnt = reinterpret_cast<int*>(ws + L.split_cnt);
     a.split_cap = L.split_cap;
-    a.ws_ml = max_parts > 1 ? reinterpret_cast<float2*>(ws + L.ml) : nullptr;
+    a.ws_ml = L.ml != 0 ? reinterpret_cast<float2*>(ws + L.ml) : nullptr;
     a.ws_acc = max_parts > 1 ? reinterpret_cast<float*>(ws + L.acc) : nullptr;
     a.num_seqs = num_seqs;
     a.num_heads = num_heads;
@@ -1509,10 +1655,15 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
     a.scale_log2 = scale * LOG2E;
     a.out_f32 = out_dtype == PA_F32;
     a.row_seq = row_seq;
+    a.ws_x = weights != nullptr ? reinterpret_cast<float*>(ws + L.x) : nullptr;
+    a.w_in = weights != nullptr ? weights->in : nullptr;
+    a.w_out = weights != nullptr ? weights->out : nullptr;
+    a.w_lens = weights != nullptr ? weights->lens : nullptr;
+    a.w_stride = weights != nullptr ? weights->stride : 0;
     // bf16 units hold up to 8 query columns per warp: up to 8 * ATTEND_WARPS /
     // group sequences sharing a partition's blocks share one unit (fp32 units
-    // are never packed)
-    a.pack = (dtype == PA_BF16 && a.group <= 8) ? 8 * ATTEND_WARPS / a.group : 1;
+    // are never packed, nor are those that keep their logits)
+    a.pack = (weights == nullptr && dtype == PA_BF16 && a.group <= 8) ? 8 * ATTEND_WARPS / a.group : 1;
     a.split_items = a.pack > 1 ? L.split_cap / num_kv_heads : 0;
     const cudaStream_t st = as_stream(stream);
     if (const int rc = device_check((phases & PA_PHASE_ATTEND) ? k_cache : context_lens)) return rc;
@@ -1529,23 +1680,7 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
         if (launch_status(e) != PA_OK) return PA_ERR_CUDA;
     }
     if (phases & PA_PHASE_ATTEND) {
-        const long long unit_bound =
-            static_cast<long long>(num_seqs) * max_parts * num_kv_heads * a.head_groups;
-        int rc;
-        if (dtype == PA_BF16) {
-            const int rb = block_size < 16 ? block_size : 16;
-            if (head_dim == 128)
-                rc = rb == 16 ? launch_attend_bf16<128, 16>(a, st, unit_bound)
-                     : rb == 8 ? launch_attend_bf16<128, 8>(a, st, unit_bound)
-                               : launch_attend_bf16<128, 4>(a, st, unit_bound);
-            else
-                rc = rb == 16 ? launch_attend_bf16<64, 16>(a, st, unit_bound)
-                     : rb == 8 ? launch_attend_bf16<64, 8>(a, st, unit_bound)
-                               : launch_attend_bf16<64, 4>(a, st, unit_bound);
-        } else {
-            rc = head_dim == 128 ? launch_attend_f32<128>(a, st, unit_bound)
-                                 : launch_attend_f32<64>(a, st, unit_bound);
-        }
+        const int rc = weights != nullptr ? launch_attend<true>(a, dtype, st) : launch_attend<false>(a, dtype, st);
         if (rc != PA_OK) return rc;
     }
     if ((phases & PA_PHASE_REDUCE) && max_parts > 1) {
@@ -1563,6 +1698,13 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
                     : launch_pdl(reduce_parts_kernel<64>, dim3(rows), dim3(REDUCE_PARTS_THREADS), 0, st, a);
         }
         if (launch_status(e) != PA_OK) return PA_ERR_CUDA;
+    }
+    if (weights != nullptr) {
+        const int chunks = (a.cap + WEIGHTS_TOKENS - 1) / WEIGHTS_TOKENS;
+        const long long ctas = static_cast<long long>(num_seqs) * num_kv_heads * chunks;
+        if (launch_status(launch_pdl(weights_kernel, dim3(static_cast<unsigned>(ctas)), dim3(WEIGHTS_THREADS), 0, st, a,
+                                     chunks)) != PA_OK)
+            return PA_ERR_CUDA;
     }
     return PA_OK;
 }
@@ -1582,6 +1724,27 @@ extern "C" int pa_decode_phases(void* out, pa_dtype out_dtype, const void* q, co
                        num_heads, num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
                        max_context_len, scale, partition_size, workspace, workspace_bytes, dtype, dev_err,
                        stream, phases, nullptr, NoPrep());
+}
+
+extern "C" size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int head_dim,
+                                                    int max_context_len, int partition_size) {
+    if (num_seqs < 0 || num_heads <= 0 || head_dim <= 0 || max_context_len < 0 || partition_size <= 0)
+        return 0;
+    return ws_layout(num_seqs, num_heads, head_dim, parts_for(max_context_len, partition_size), max_context_len).total;
+}
+
+extern "C" int pa_decode_weights(void* out, pa_dtype out_dtype, float* weights_out, const float* weights_in,
+                                 const int32_t* weights_lens, int weights_stride, const void* q,
+                                 const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                 const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                 int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                                 int max_context_len, float scale, int partition_size, void* workspace,
+                                 size_t workspace_bytes, pa_dtype dtype, int32_t* dev_err, pa_stream stream) {
+    const WeightArgs w{weights_in, weights_out, weights_lens, weights_stride};
+    return decode_impl(out, out_dtype, q, k_cache, v_cache, block_tables, context_lens, num_seqs, num_heads,
+                       num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq, max_context_len, scale,
+                       partition_size, workspace, workspace_bytes, dtype, dev_err, stream, PA_PHASE_ALL, nullptr,
+                       NoPrep(), nullptr, 0, &w);
 }
 
 static size_t prefill_rows_bytes(int num_tokens) {

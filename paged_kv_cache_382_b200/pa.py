@@ -43,6 +43,12 @@ SIGNATURES = {
                         _i, _vp, _sz, _i, _i32p, _vp]),
     "pa_decode_noalloc": (_i, [_vp, _i, _vp, _vp, _vp, _i32p, _i32p, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                _i, _i, _i32p, _vp]),
+    "pa_decode_weights_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "pa_decode_weights": (_i, [_vp, _i, _vp, _vp, _i32p, _i, _vp, _vp, _vp, _i32p, _i32p, _i, _i, _i, _i, _i, _i, _i,
+                               _i, _f, _i, _vp, _sz, _i, _i32p, _vp]),
+    "pa_select_tokens": (_i, [_i32p, _i32p, _vp, _i32p, _i32p, _i, _i, _i, _i, _i, _i32p, _vp]),
+    "pa_compact": (_i, [_vp, _vp, _vp, _vp, _i, _i32p, _i32p, _i, _i, _i32p, _i, _i, _i32p, _i32p, _i, _i, _i, _i, _i,
+                        _i, _i32p, _vp]),
     "pa_bm_create": (ctypes.c_void_p, [_i, _i, _vp, _i]),
     "pa_bm_destroy": (None, [_vp]),
     "pa_bm_add_sequence": (_i, [_vp, ctypes.c_int64]),
@@ -52,6 +58,7 @@ SIGNATURES = {
                           ctypes.POINTER(ctypes.c_int)]),
     "pa_bm_append_batch": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _i, ctypes.POINTER(ctypes.c_int),
                                 ctypes.POINTER(ctypes.c_int)]),
+    "pa_bm_compact": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(ctypes.c_int)]),
     "pa_bm_block_table": (_i, [_vp, ctypes.c_int64, _vp, _i, ctypes.POINTER(ctypes.c_int),
                                ctypes.POINTER(ctypes.c_int64)]),
     "pa_bm_num_free": (_i, [_vp]),
@@ -289,6 +296,112 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_dst_pairs: tor
     _check(rc, "pa_copy_blocks")
 
 
+def alloc_weights_workspace(num_seqs: int, num_heads: int, head_dim: int, capacity: int,
+                            partition_size: int = 512, device=None) -> torch.Tensor:
+    """Workspace of ``decode_weights`` for contexts up to ``capacity`` tokens."""
+    n = lib.pa_decode_weights_workspace_bytes(num_seqs, num_heads, head_dim, capacity, partition_size)
+    if n == 0:
+        raise ValueError("invalid arguments for pa_decode_weights_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def decode_weights(out: torch.Tensor, weights_out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, *,
+                   weights_in: Optional[torch.Tensor] = None, weights_lens: Optional[torch.Tensor] = None,
+                   max_context_len: int = 0, partition_size: int = 512, workspace: Optional[torch.Tensor] = None,
+                   dev_err: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Paged decode attention that also adds every cached token's attention weight, summed over the
+    query heads of its kv head, to its running total: ``weights_out`` = ``weights_in`` (fp32
+    [S][Hkv][stride], or None: zeros; may be ``weights_out``) + the step's weights.  Writes and
+    returns ``out`` [S][Hq][d]."""
+    NB, Hkv, B, d = k_cache.shape
+    S, Hq, dq = q.shape
+    if dq != d or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("q / out must be [num_seqs][num_heads][head_dim] over the pool's head_dim")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or tuple(context_lens.shape) != (S,):
+        raise ValueError("block_tables must be [num_seqs][max_blocks] and context_lens [num_seqs]")
+    if weights_out.dim() != 3 or tuple(weights_out.shape[:2]) != (S, Hkv):
+        raise ValueError("weights_out must be [num_seqs][num_kv_heads][stride]")
+    if weights_in is not None and weights_in.shape != weights_out.shape:
+        raise ValueError("weights_in and weights_out must have the same shape")
+    if weights_lens is not None and tuple(weights_lens.shape) != (S,):
+        raise ValueError("weights_lens must be [num_seqs]")
+    dt = k_cache.dtype
+    if workspace is None:
+        cap = decode_capacity(block_tables, B, max_context_len)
+        workspace = alloc_weights_workspace(S, Hq, d, cap, partition_size, q.device)
+    f32 = torch.float32
+    rc = lib.pa_decode_weights(
+        _dev(out, "out"), dtype_code(out.dtype), _dev(weights_out, "weights_out", f32),
+        None if weights_in is None else _dev(weights_in, "weights_in", f32),
+        None if weights_lens is None else _dev(weights_lens, "weights_lens", torch.int32), weights_out.shape[2],
+        _dev(q, "q", dt), _dev(k_cache, "k_cache", dt), _dev(v_cache, "v_cache", dt),
+        _dev(block_tables, "block_tables", torch.int32), _dev(context_lens, "context_lens", torch.int32), S, Hq, Hkv, d,
+        B, NB, block_tables.shape[1], max_context_len, float(scale), partition_size,
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), dtype_code(dt), _opt_err(dev_err),
+        _stream_handle(stream))
+    _check(rc, "pa_decode_weights")
+    return out
+
+
+def select_tokens(keep: torch.Tensor, keep_lens: torch.Tensor, weights: torch.Tensor, context_lens: torch.Tensor,
+                  budgets: torch.Tensor, *, recent: int = 0, dev_err: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Positions to keep of each sequence and kv head: the last ``recent`` ones and those with the
+    largest totals (``weights`` fp32 [S][Hkv][stride]) up to ``budgets`` (int32 [S]), ascending, into
+    ``keep`` (int32 [S][Hkv][width]) and their number into ``keep_lens`` (int32 [S])."""
+    if weights.dim() != 3 or keep.dim() != 3 or keep.shape[:2] != weights.shape[:2]:
+        raise ValueError("weights must be [num_seqs][num_kv_heads][stride] and keep [num_seqs][num_kv_heads][width]")
+    S, Hkv, stride = weights.shape
+    if tuple(keep_lens.shape) != (S,) or tuple(context_lens.shape) != (S,) or tuple(budgets.shape) != (S,):
+        raise ValueError("keep_lens, context_lens and budgets must be [num_seqs]")
+    i32 = torch.int32
+    rc = lib.pa_select_tokens(
+        _dev(keep, "keep", i32), _dev(keep_lens, "keep_lens", i32), _dev(weights, "weights", torch.float32),
+        _dev(context_lens, "context_lens", i32), _dev(budgets, "budgets", i32), S, Hkv, stride, keep.shape[2],
+        int(recent), _opt_err(dev_err), _stream_handle(stream))
+    _check(rc, "pa_select_tokens")
+    return keep
+
+
+def compact(k_cache: torch.Tensor, v_cache: torch.Tensor, src_tables: torch.Tensor, dst_tables: torch.Tensor,
+            keep: torch.Tensor, keep_lens: torch.Tensor, *, starts: Optional[torch.Tensor] = None,
+            weights_in: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+            dev_err: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Move the kept tokens' K, V (and totals) to consecutive positions: position ``keep[s][h][j]``
+    (through ``src_tables``) goes to ``starts[s] + j`` (through ``dst_tables``, which may be
+    ``src_tables``).  ``keep`` is int32 [S][Hkv][width], or [S][1][width] for the same positions in
+    every kv head; ``starts`` None means 0."""
+    NB, Hkv, B, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must match")
+    S = keep_lens.shape[0]
+    if keep.dim() != 3 or keep.shape[0] != S or keep.shape[1] not in (1, Hkv):
+        raise ValueError("keep must be [num_seqs][num_kv_heads or 1][width] and keep_lens [num_seqs]")
+    if src_tables.dim() != 2 or dst_tables.dim() != 2 or src_tables.shape[0] != S or dst_tables.shape[0] != S:
+        raise ValueError("src_tables and dst_tables must be [num_seqs][max_blocks]")
+    if starts is not None and tuple(starts.shape) != (S,):
+        raise ValueError("starts must be [num_seqs]")
+    if (weights_in is None) != (weights_out is None):
+        raise ValueError("weights_in and weights_out come together")
+    stride = 0
+    if weights_in is not None:
+        if weights_in.dim() != 3 or tuple(weights_in.shape[:2]) != (S, Hkv) or weights_in.shape != weights_out.shape:
+            raise ValueError("weights_in and weights_out must be [num_seqs][num_kv_heads][stride]")
+        stride = weights_in.shape[2]
+    i32, f32, dt = torch.int32, torch.float32, k_cache.dtype
+    rc = lib.pa_compact(
+        _dev(k_cache, "k_cache", dt), _dev(v_cache, "v_cache", dt),
+        None if weights_out is None else _dev(weights_out, "weights_out", f32),
+        None if weights_in is None else _dev(weights_in, "weights_in", f32), stride,
+        _dev(src_tables, "src_tables", i32), _dev(dst_tables, "dst_tables", i32), src_tables.shape[1],
+        dst_tables.shape[1], _dev(keep, "keep", i32), keep.shape[1], keep.shape[2],
+        None if starts is None else _dev(starts, "starts", i32), _dev(keep_lens, "keep_lens", i32), S, Hkv, d, B, NB,
+        dtype_code(dt), _opt_err(dev_err), _stream_handle(stream))
+    _check(rc, "pa_compact")
+
+
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 
@@ -397,6 +510,29 @@ class NativeBlockManager:
         _check(rc, "pa_bm_append_batch")
         pairs = [(int(copies[2 * i]), int(copies[2 * i + 1])) for i in range(ncopies.value)]
         return slots[:total], pairs, ncached.value
+
+    def compact(self, seq_ids, unchanged, num_tokens, token_ids=None):
+        """Bookkeeping of one ``compact`` call: seq_ids[k] keeps num_tokens[k] tokens, the first
+        unchanged[k] of them in place.  token_ids (prefix caching): the ids of the others, all
+        sequences' in a row, or None if unknown.  Returns the [(src, dst)] block copies to run
+        before the moves."""
+        np = self._np
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        u = np.ascontiguousarray(unchanged, dtype=np.int64)
+        n = np.ascontiguousarray(num_tokens, dtype=np.int64)
+        if not ids.shape == u.shape == n.shape or ids.ndim != 1:
+            raise ValueError("seq_ids, unchanged and num_tokens must be one value per sequence")
+        toks = None
+        if token_ids is not None:
+            toks = np.ascontiguousarray(token_ids, dtype=np.int32)
+            if toks.size != int((n - u).sum()):
+                raise ValueError("token_ids must hold sum(num_tokens - unchanged) ids")
+        copies = np.empty(2 * max(len(ids), 1), dtype=np.int64)
+        ncopies = ctypes.c_int(0)
+        rc = lib.pa_bm_compact(self._h, len(ids), ids.ctypes.data, u.ctypes.data, n.ctypes.data,
+                               None if toks is None else toks.ctypes.data, copies.ctypes.data, ctypes.byref(ncopies))
+        _check(rc, "pa_bm_compact")
+        return [(int(copies[2 * i]), int(copies[2 * i + 1])) for i in range(ncopies.value)]
 
     def block_table(self, seq_id: int):
         np = self._np
