@@ -306,6 +306,59 @@ PA_API int pa_decode_noalloc(void* out, pa_dtype out_dtype, const void* q, const
                       int partition_size, pa_dtype dtype, int32_t* dev_err, pa_stream stream);
 
 /*
+ * pa_tree_decode -- attention of drafted tokens against the paged context: the
+ * verification step of speculative decoding.  The drafted tokens ("nodes") of a
+ * sequence form a tree; all of them are in the pool already, behind the prefix
+ * (write them with pa_reshape_and_cache first), and all are verified at once.
+ * Node i of sequence s (of n_s = query_start[s+1] - query_start[s]) sits at position
+ * context_lens[s] - n_s + i and attends to every position below
+ * context_lens[s] - n_s and to the nodes its mask row names (its ancestors and
+ * itself, as pa_tree_mask fills it; any other set is as good).
+ *
+ *   q, out        [num_tokens][num_heads][head_dim]: the nodes of all sequences, sequence s
+ *                 owning rows query_start[s] .. query_start[s+1]-1
+ *   query_start   int32 [num_seqs + 1] (device), as for pa_prefill; rows of a sequence whose
+ *                 range is malformed are left as they were (PA_DEVERR_CONTEXT), as are
+ *                 rows behind the last sequence's
+ *   context_lens  int32 [num_seqs]: tokens of each sequence in the pool, its nodes included
+ *   tree_mask     int64 [num_tokens][mask_words] (device): bit j % 64 of word j / 64 of a
+ *                 node's row says whether it sees node j of its sequence.  Bits past n_s are
+ *                 ignored.  1 <= mask_words <= PA_TREE_MAX_WORDS; a sequence with more than
+ *                 64 * mask_words nodes is flagged (PA_DEVERR_CONTEXT) and nobody sees the
+ *                 nodes past that.
+ *   workspace     pa_tree_workspace_bytes(num_tokens, num_heads, head_dim) bytes, 256-byte
+ *                 aligned, whatever the contexts; its contents need no initialisation
+ * A row that sees nothing is zero.  More nodes than context: PA_DEVERR_CONTEXT, positions
+ * below zero do not exist.  Other arguments and errors as for pa_decode.
+ * Arithmetic: as for pa_decode.  The work is cut over the GPU by the whole batch, so the same
+ * call gives the same bits every time, but a sequence's rounding may differ in another batch.
+ * On bf16 pools with block_size 8, 16 or 32 (pa_tree_uses_tensor_cores) the products run as
+ * tcgen05 MMAs over tiles of 128 query rows; elsewhere on the CUDA cores in fp32.  On the
+ * tensor cores every K/V value in the context must be finite: a non-finite value reaches
+ * every row of its sequence and kv head (0 * NaN), whether the row sees that token or not.
+ * Launches two kernels (attention, join) on `stream`.
+ */
+#define PA_TREE_MAX_WORDS 8   /* 512 nodes per sequence */
+PA_API size_t pa_tree_workspace_bytes(int num_tokens, int num_heads, int head_dim);
+/* 1 if pa_tree_decode serves such a pool on the tensor cores, 0 if on the CUDA cores. */
+PA_API int pa_tree_uses_tensor_cores(pa_dtype dtype, int block_size);
+PA_API int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                          const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+                          const int32_t* query_start, const int64_t* tree_mask, int mask_words, int num_seqs,
+                          int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                          int num_blocks, int max_blocks_per_seq, int max_context_len, float scale,
+                          void* workspace, size_t workspace_bytes, pa_dtype dtype, int32_t* dev_err,
+                          pa_stream stream);
+/*
+ * pa_tree_mask -- mask rows of one tree (host memory, no CUDA call): parents[num_nodes]
+ * names each node's parent, a node before it, or < 0 where it follows the prefix;
+ * mask[num_nodes][mask_words] receives each node's ancestors and itself.
+ * PA_ERR_INVALID_ARG for a parent that is not before its node, PA_ERR_UNSUPPORTED for more
+ * nodes than mask_words hold.
+ */
+PA_API int pa_tree_mask(const int32_t* parents, int num_nodes, int mask_words, int64_t* mask);
+
+/*
  * pa_decode_weights -- pa_decode that also keeps, for each cached token, the
  * running total of the attention weight it has received: what an eviction
  * chooses by (pa_select_tokens).  With p_nj the softmax weight of query head n

@@ -1,0 +1,444 @@
+// tree_decode.cu -- pa_tree_decode: attention of a tree of drafted tokens over
+// a paged cache.  The entry point, the attend kernel on the CUDA cores (fp32
+// pools, and bf16 pools of 4-token blocks), the join of cut units, and the
+// host-side construction of masks from parents (pa_tree_mask).  tree.cuh says
+// what is computed and how the work is cut.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <climits>
+#include <cmath>
+
+#include "pa_device.cuh"
+#include "pa_host.h"
+#include "tree.cuh"
+
+namespace pa {
+namespace {
+
+// ---------------------------------------------------------------------------
+// attend on the CUDA cores
+//
+// Bound by fp32 FMAs (4 rows d per token and kv head).  256 threads, 16 x 16:
+// thread (ty, tx) holds rows 4 ty .. 4 ty + 3 of S for tokens 4 tx .. and of O
+// for D / 16 columns, so each operand read from shared memory feeds four FMAs.
+// Q and K are stored transposed ([d][row]) for that; softmax statistics of a row
+// live in the 16 threads that share it.
+// ---------------------------------------------------------------------------
+
+constexpr int TS_ROWS = 64;
+constexpr int TS_KT = 64;
+constexpr int TS_THREADS = 256;
+constexpr int TS_PAD = 68;   // floats per transposed row: 16-byte aligned, columns spread over the banks
+
+template <int D>
+constexpr int tree_simt_smem() {
+    return (2 * D * TS_PAD + TS_KT * D + TS_ROWS * TS_PAD) * 4;
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+    return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(TS_THREADS) tree_simt_kernel(const TreeArgs a) {
+    constexpr int OC = D / 16;   // output columns per thread
+    extern __shared__ __align__(16) uint8_t smem_dyn[];
+    float* sQ = reinterpret_cast<float*>(smem_dyn);   // [D][TS_PAD]
+    float* sK = sQ + D * TS_PAD;                      // [D][TS_PAD]
+    float* sV = sK + D * TS_PAD;                      // [TS_KT][D]
+    float* sP = sV + TS_KT * D;                       // [TS_ROWS][TS_PAD]
+    __shared__ int s_row[TS_KT];                      // pool row of each token of the tile, or -1
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const T* q = static_cast<const T*>(a.q);
+    const T* kc = static_cast<const T*>(a.k_cache);
+    const T* vc = static_cast<const T*>(a.v_cache);
+    pdl_wait();
+    pdl_launch_dependents();
+    TreeWalker<TS_ROWS, TS_KT> walk;
+    tree_begin(a, reinterpret_cast<long long*>(smem_dyn), walk);
+    __syncthreads();
+
+    TreeRun r;
+    while (walk.next(a, r)) {
+        if (r.starts && tid == 0) tree_record(a, r);
+        // Q, scaled into the log2 domain
+        for (int i = tid; i < TS_ROWS * (D / 4); i += TS_THREADS) {
+            const int row = i % TS_ROWS, c = i / TS_ROWS * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < r.rows) v = load4<T>(q + tree_out_row(a, r.first, r.kvh, r.row0 + row) * D + c);
+            sQ[(c + 0) * TS_PAD + row] = v.x;
+            sQ[(c + 1) * TS_PAD + row] = v.y;
+            sQ[(c + 2) * TS_PAD + row] = v.z;
+            sQ[(c + 3) * TS_PAD + row] = v.w;
+        }
+        const uint32_t* mrow[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mrow[i] = a.tree_mask + static_cast<size_t>(r.first + min(r.n - 1, (r.row0 + 4 * ty + i) / a.group)) * a.mask_words32;
+        const int pre = r.ctx - r.n;   // positions below it: the prefix
+        float m[4], l[4], o[4][OC];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = NEG_INF;
+            l[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < OC; ++j) o[i][j] = 0.f;
+        }
+        for (int t = r.t0; t < r.t1; ++t) {
+            const int p0 = t * TS_KT;
+            __syncthreads();   // the previous tile is no longer read
+            if (tid < TS_KT) {
+                int at = -1;
+                if (p0 + tid < r.ctx) {
+                    const int b = a.block_tables[static_cast<size_t>(r.s) * a.max_blocks + ((p0 + tid) >> a.log2_block)];
+                    if (b < 0 || b >= a.num_blocks)
+                        flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
+                    else
+                        at = (b * a.num_kv_heads + r.kvh) * a.block_size + ((p0 + tid) & (a.block_size - 1));
+                }
+                s_row[tid] = at;
+            }
+            __syncthreads();
+            for (int i = tid; i < TS_KT * (D / 4); i += TS_THREADS) {
+                const int tok = i % TS_KT, c = i / TS_KT * 4;
+                const int at = s_row[tok];
+                float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (at >= 0) k4 = load4<T>(kc + static_cast<size_t>(at) * D + c);
+                sK[(c + 0) * TS_PAD + tok] = k4.x;
+                sK[(c + 1) * TS_PAD + tok] = k4.y;
+                sK[(c + 2) * TS_PAD + tok] = k4.z;
+                sK[(c + 3) * TS_PAD + tok] = k4.w;
+            }
+            for (int i = tid; i < TS_KT * (D / 4); i += TS_THREADS) {
+                const int tok = i / (D / 4), c = i % (D / 4) * 4;
+                const int at = s_row[tok];
+                float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);   // tokens that take no part: 0 * 0
+                if (at >= 0) v4 = load4<T>(vc + static_cast<size_t>(at) * D + c);
+                *reinterpret_cast<float4*>(sV + tok * D + c) = v4;
+            }
+            __syncthreads();
+            float x[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+#pragma unroll 4
+            for (int d = 0; d < D; ++d) {
+                const float4 qv = *reinterpret_cast<const float4*>(sQ + d * TS_PAD + 4 * ty);
+                const float4 kv = *reinterpret_cast<const float4*>(sK + d * TS_PAD + 4 * tx);
+                const float qa[4] = {qv.x, qv.y, qv.z, qv.w}, ka[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[i][j] = fmaf(qa[i], ka[j], x[i][j]);
+            }
+            uint32_t in = 0;   // tokens of this thread that take part
+#pragma unroll
+            for (int j = 0; j < 4; ++j) in |= (s_row[4 * tx + j] >= 0 ? 1u : 0u) << j;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t seen = in & tree_bits(mrow[i], a.mask_words32, p0 + 4 * tx - pre);
+                float mx = NEG_INF;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i][j] = (seen >> j) & 1u ? x[i][j] * a.scale_log2 : NEG_INF;
+                    mx = fmaxf(mx, x[i][j]);
+                }
+#pragma unroll
+                for (int off = 1; off < 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, off));
+                const float mn = fmaxf(m[i], mx);
+                const float base = mn == NEG_INF ? 0.f : mn;
+                const float al = exp2_approx(m[i] - base);
+                m[i] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i][j] = exp2_approx(x[i][j] - base);
+                    sum += x[i][j];
+                }
+#pragma unroll
+                for (int off = 1; off < 16; off <<= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
+                l[i] = fmaf(l[i], al, sum);
+#pragma unroll
+                for (int j = 0; j < OC; ++j) o[i][j] *= al;
+                *reinterpret_cast<float4*>(sP + (4 * ty + i) * TS_PAD + 4 * tx) =
+                    make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+            }
+            __syncwarp();   // a row's 16 threads share a warp
+#pragma unroll 2
+            for (int tok = 0; tok < TS_KT; tok += 4) {
+                float p[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 v = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * TS_PAD + tok);
+                    p[i][0] = v.x;
+                    p[i][1] = v.y;
+                    p[i][2] = v.z;
+                    p[i][3] = v.w;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int j = 0; j < OC; j += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(sV + (tok + k) * D + 16 * j + 4 * tx);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // a token the row does not see adds nothing, whatever its value
+                            if (p[i][k] != 0.f) {
+                                o[i][j + 0] = fmaf(p[i][k], v.x, o[i][j + 0]);
+                                o[i][j + 1] = fmaf(p[i][k], v.y, o[i][j + 1]);
+                                o[i][j + 2] = fmaf(p[i][k], v.z, o[i][j + 2]);
+                                o[i][j + 3] = fmaf(p[i][k], v.w, o[i][j + 3]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        const bool whole = r.t0 == 0 && r.t1 == r.nt;
+        const int slot = 2 * blockIdx.x + (r.starts ? 0 : 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * ty + i;
+            if (row >= r.rows) continue;
+            if (whole) {
+                const size_t at = tree_out_row(a, r.first, r.kvh, r.row0 + row) * D;
+                const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+#pragma unroll
+                for (int j = 0; j < OC; j += 4) {
+                    const int c = 16 * j + 4 * tx;
+                    if (a.out_f32)
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + c) =
+                            make_float4(o[i][j] * inv, o[i][j + 1] * inv, o[i][j + 2] * inv, o[i][j + 3] * inv);
+                    else
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at + c) =
+                            make_uint2(pack_bf16(o[i][j] * inv, o[i][j + 1] * inv),
+                                       pack_bf16(o[i][j + 2] * inv, o[i][j + 3] * inv));
+                }
+            } else {
+                float4* acc = reinterpret_cast<float4*>(tree_part(a, slot, D));
+#pragma unroll
+                for (int j = 0; j < OC; j += 4)
+                    acc[(4 * j + tx) * a.part_rows + row] = make_float4(o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]);
+                if (tx == 0) a.part_ml[static_cast<size_t>(slot) * a.part_rows + row] = make_float2(m[i], l[i]);
+            }
+        }
+        __syncthreads();   // sQ and sP are written again for the next run
+    }
+}
+
+template <int D, typename T>
+int launch_tree_simt(const TreeArgs& a, int ctas, cudaStream_t st) {
+    static KernelSlot slot;
+    auto kern = tree_simt_kernel<D, T>;
+    if (prepare_kernel(slot, reinterpret_cast<const void*>(kern), TS_THREADS, tree_simt_smem<D>()) <= 0) return PA_ERR_CUDA;
+    return launch_status(launch_pdl(kern, dim3(ctas), dim3(TS_THREADS), tree_simt_smem<D>(), st, a));
+}
+
+// ---------------------------------------------------------------------------
+// join: the partials of each unit that the shares cut, in CTA order.  The
+// unit's first cut lies at the start of some CTA's share: that CTA's row of
+// the grid joins it.
+// ---------------------------------------------------------------------------
+
+constexpr int TJ_THREADS = 128;
+constexpr int TJ_ROWS = 32;   // rows per CTA
+
+template <int D>
+__global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const TreeArgs a, int ctas) {
+    __shared__ float s_coef[TJ_ROWS][TREE_CTAS_MAX + 1];   // weight of each partial, then 1 / sum
+    pdl_wait();
+    pdl_launch_dependents();
+    const int c = blockIdx.x + 1;   // share 0 starts no cut
+    const long long W = *a.line;
+    const int g = static_cast<int>(W < ctas ? W : ctas);
+    if (c >= g) return;
+    const int4 r0 = a.recs[2 * c], r1 = a.recs[2 * c + 1];
+    const int t0 = r1.x, nt = r1.y, rows = r0.w;
+    if (t0 == 0) return;                             // the share starts at a unit's start
+    const long long begin = tree_share(W, ctas, c) - t0, end = begin + nt;
+    if (tree_share(W, ctas, c - 1) > begin) return;  // not the unit's first cut
+    const int row0 = blockIdx.y * TJ_ROWS, here = min(TJ_ROWS, rows - row0);
+    if (here <= 0) return;
+    int last = c;
+    while (last + 1 < g && tree_share(W, ctas, last + 1) < end) ++last;
+    // partials: CTA c - 1's (its first run if its share starts with the unit), then those of c .. last
+    const int head = 2 * (c - 1) + (tree_share(W, ctas, c - 1) == begin ? 0 : 1);
+    const int parts = last - c + 2;
+    auto slot_of = [&](int p) { return p == 0 ? head : 2 * (c - 1 + p); };
+    if (threadIdx.x < here) {
+        const int row = row0 + threadIdx.x;
+        float M = NEG_INF, L = 0.f;
+        for (int p = 0; p < parts; ++p)
+            M = fmaxf(M, a.part_ml[static_cast<size_t>(slot_of(p)) * a.part_rows + row].x);
+        for (int p = 0; p < parts; ++p) {
+            const float2 ml = a.part_ml[static_cast<size_t>(slot_of(p)) * a.part_rows + row];
+            const float e = M == NEG_INF ? 0.f : exp2_approx(ml.x - M);
+            s_coef[threadIdx.x][p] = e;
+            L = fmaf(e, ml.y, L);
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        for (int p = 0; p < parts; ++p) s_coef[threadIdx.x][p] *= inv;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < TJ_ROWS * (D / 4); i += TJ_THREADS) {
+        const int rr = i % TJ_ROWS, c4 = i / TJ_ROWS;
+        if (rr >= here) continue;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < parts; ++p) {
+            const float e = s_coef[rr][p];
+            const float4 v = reinterpret_cast<const float4*>(tree_part(a, slot_of(p), D))[c4 * a.part_rows + row0 + rr];
+            o.x = fmaf(e, v.x, o.x);
+            o.y = fmaf(e, v.y, o.y);
+            o.z = fmaf(e, v.z, o.z);
+            o.w = fmaf(e, v.w, o.w);
+        }
+        const size_t at = tree_out_row(a, r0.x, r0.y, r0.z + row0 + rr) * D + 4 * c4;
+        if (a.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
+        else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct TreeWs {
+    size_t line, recs, ml, acc, total;
+    int rows;
+};
+
+inline TreeWs tree_ws(long long num_tokens, int num_heads, int head_dim) {
+    TreeWs w;
+    const int most = tree_tc_rows() > TS_ROWS ? tree_tc_rows() : TS_ROWS;
+    const long long rows = num_tokens * num_heads;   // no unit has more
+    w.rows = static_cast<int>(rows < most ? rows : most);
+    w.line = 0;
+    w.recs = 256;
+    w.ml = w.recs + up256(2 * TREE_CTAS_MAX * sizeof(int4));
+    w.acc = w.ml + up256(2 * TREE_CTAS_MAX * static_cast<size_t>(w.rows) * sizeof(float2));
+    w.total = w.acc + up256(2 * TREE_CTAS_MAX * static_cast<size_t>(w.rows) * head_dim * sizeof(float));
+    return w;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_tree_workspace_bytes(int num_tokens, int num_heads, int head_dim) {
+    if (num_tokens < 0 || num_heads <= 0 || head_dim <= 0) return 0;
+    return tree_ws(num_tokens, num_heads, head_dim).total;
+}
+
+extern "C" int pa_tree_uses_tensor_cores(pa_dtype dtype, int block_size) { return tree_tc_eligible(dtype, block_size) ? 1 : 0; }
+
+extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_start,
+                              const int64_t* tree_mask, int mask_words, int num_seqs, int num_tokens, int num_heads,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                              int max_context_len, float scale, void* workspace, size_t workspace_bytes, pa_dtype dtype,
+                              int32_t* dev_err, pa_stream stream) {
+    if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0 || max_context_len < 0 || num_heads % num_kv_heads != 0 || !valid_dtype(dtype) ||
+        !valid_dtype(out_dtype) || !std::isfinite(scale))
+        return PA_ERR_INVALID_ARG;
+    if (out_dtype != PA_F32 && out_dtype != dtype) return PA_ERR_UNSUPPORTED;
+    if (!(head_dim == 64 || head_dim == 128)) return PA_ERR_UNSUPPORTED;
+    if (!(block_size == 4 || block_size == 8 || block_size == 16 || block_size == 32)) return PA_ERR_UNSUPPORTED;
+    if (mask_words < 1) return PA_ERR_INVALID_ARG;
+    if (mask_words > PA_TREE_MAX_WORDS) return PA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * num_kv_heads * block_size > INT_MAX ||
+        static_cast<long long>(num_tokens) * num_heads > INT_MAX || num_seqs > 32 * TREE_WINDOWS_MAX)
+        return PA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (num_seqs == 0) return PA_ERR_INVALID_ARG;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !tree_mask || !workspace)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) ||
+        !aligned_to(block_tables, 4) || !aligned_to(context_lens, 4) || !aligned_to(query_start, 4) ||
+        !aligned_to(tree_mask, 8) || !aligned_to(workspace, 256))
+        return PA_ERR_INVALID_ARG;
+    const TreeWs L = tree_ws(num_tokens, num_heads, head_dim);
+    if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
+
+    long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
+    if (max_context_len > 0 && max_context_len < cap) cap = max_context_len;
+    TreeArgs a;
+    a.out = out;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
+    a.dev_err = dev_err;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.line = reinterpret_cast<long long*>(ws + L.line);
+    a.recs = reinterpret_cast<int4*>(ws + L.recs);
+    a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+    a.part_acc = reinterpret_cast<float*>(ws + L.acc);
+    a.part_rows = L.rows;
+    a.mask_words32 = 2 * mask_words;
+    a.num_seqs = num_seqs;
+    a.num_tokens = num_tokens;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.group = num_heads / num_kv_heads;
+    a.block_size = block_size;
+    a.log2_block = block_size == 4 ? 2 : block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
+    a.num_blocks = num_blocks;
+    a.max_blocks = max_blocks_per_seq;
+    a.cap = static_cast<int>(cap);
+    a.scale_log2 = scale * LOG2E;
+    a.out_f32 = out_dtype == PA_F32;
+    const cudaStream_t st = as_stream(stream);
+    if (const int rc = device_check(k_cache)) return rc;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    const int ctas = sms < TREE_CTAS_MAX ? sms : TREE_CTAS_MAX;
+    int rc;
+    if (tree_tc_eligible(dtype, block_size))
+        rc = launch_tree_tc(a, head_dim, ctas, st);
+    else if (dtype == PA_F32)
+        rc = head_dim == 128 ? launch_tree_simt<128, float>(a, ctas, st) : launch_tree_simt<64, float>(a, ctas, st);
+    else
+        rc = head_dim == 128 ? launch_tree_simt<128, __nv_bfloat16>(a, ctas, st)
+                             : launch_tree_simt<64, __nv_bfloat16>(a, ctas, st);
+    if (rc != PA_OK || ctas < 2) return rc;
+    const dim3 grid(ctas - 1, (L.rows + TJ_ROWS - 1) / TJ_ROWS);
+    return launch_status(head_dim == 128 ? launch_pdl(tree_join_kernel<128>, grid, dim3(TJ_THREADS), 0, st, a, ctas)
+                                         : launch_pdl(tree_join_kernel<64>, grid, dim3(TJ_THREADS), 0, st, a, ctas));
+}
+
+extern "C" int pa_tree_mask(const int32_t* parents, int num_nodes, int mask_words, int64_t* mask) {
+    if (num_nodes < 0 || mask_words < 1) return PA_ERR_INVALID_ARG;
+    if (mask_words > PA_TREE_MAX_WORDS || num_nodes > 64 * mask_words) return PA_ERR_UNSUPPORTED;
+    if (num_nodes > 0 && (!parents || !mask)) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < num_nodes; ++i)
+        if (parents[i] >= i) return PA_ERR_INVALID_ARG;   // parents come first
+    for (int i = 0; i < num_nodes; ++i) {
+        uint64_t* row = reinterpret_cast<uint64_t*>(mask) + static_cast<size_t>(i) * mask_words;
+        const uint64_t* up = parents[i] >= 0 ? reinterpret_cast<const uint64_t*>(mask) + static_cast<size_t>(parents[i]) * mask_words : nullptr;
+        for (int w = 0; w < mask_words; ++w) row[w] = up ? up[w] : 0u;
+        row[i / 64] |= 1ull << (i % 64);
+    }
+    return PA_OK;
+}

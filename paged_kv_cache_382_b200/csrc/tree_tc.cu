@@ -1,0 +1,565 @@
+// tree_tc.cu -- attention of drafted tokens over a paged cache on the
+// 5th-generation tensor cores (bf16 pools; tree.cuh says what is computed and
+// how the work is cut into shares).
+//
+// One CTA per SM takes a share of the work line.  A unit's rows are one or two
+// MMA tiles of 128 rows; K and V come in tiles of 128 tokens.  Two streams,
+// each with its own four softmax warps, S / P buffer and O accumulator in
+// tensor memory, keep the tensor cores and the exponentials busy at once:
+//   more than 128 rows: stream w owns row tile w and takes every K/V tile, so
+//                       K and V are read once for up to 256 rows;
+//   up to 128 rows:     both streams hold the same rows, stream w takes the run's
+//                       tiles w, w + 2, ...; the epilogue joins the two.
+// Step i of a run (stream i % 2) is
+//   S = Q . K^T   (M = 128 rows, N = 128 tokens, K = d)
+//   softmax       (online, base 2, lazy rescale of O in tensor memory)
+//   O += P . V    (M = 128, N = d, K = 128 tokens; P as a bf16 pair hi + lo,
+//                  written over S: about 16 significant bits, so that the
+//                  weights' rounding stays below the output's)
+// and the MMA thread issues PV(i), S(i + 2) while the other stream's warps
+// work on step i + 1.
+//
+// K and V tiles go through one ring of five 32 KB slots in the order K0 V0 K1
+// V1 ...; a K slot is free again once its S is done, so up to 160 KB are in
+// flight or in use.  The loader warp runs ahead into the CTA's next runs; one
+// lane per block issues that block's bulk copies.
+//
+// Per 128-token tile: 64 KB of K and V, 1.5 us at an SM's share of the measured
+// copy bandwidth; per step 512 + 1024 tensor cycles and, on each SM quarter,
+// 1024 cycles of exponentials.  Up to 128 rows one step per tile leaves the
+// kernel bound by HBM; 256 rows take two steps, 1.6 us of MMAs, about the same.
+//
+// Every wait is bounded: on a timeout the CTA raises PA_DEVERR_TIMEOUT, skips
+// what is left, lets its copies and MMAs drain, frees its tensor memory and
+// returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+#include "pa_host.h"
+#include "pa_tma.h"
+#include "pa_umma.cuh"
+#include "tree.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int TT_M = 128;               // rows of a stream: the MMA's M
+constexpr int TT_ROWS = 2 * TT_M;       // rows of a unit
+constexpr int TT_KT = 128;              // tokens of a K or V tile
+constexpr int TT_SLOTS = 5;             // ring slots (one K or V tile each)
+constexpr int TT_MASKS = 4;             // tiles whose token masks are kept
+constexpr int TT_SOFTMAX_WARPS = 8;     // warps 0-3: stream 0, 4-7: stream 1
+constexpr int TT_SOFTMAX = TT_SOFTMAX_WARPS * 32;
+constexpr int TT_MMA_WARP = 8;
+constexpr int TT_LOAD_WARP = 9;
+constexpr int TT_THREADS = (TT_SOFTMAX_WARPS + 2) * 32;
+constexpr int TT_TMEM_COLS = 512;
+constexpr int TT_Q_BARRIER = 1;         // Q in shared memory, O read: softmax + MMA warps
+constexpr int TT_ML_BARRIER = 2;        // the streams' (max, sum) exchanged: softmax warps
+constexpr int TT_SEQ_WORDS = TT_KT / 32;
+
+template <int D>
+struct TreeGeom {
+    static constexpr int NH = D / 64;
+    static constexpr int Q_HALF = TT_M * 128;          // 128 rows x 64 columns, 128-byte swizzle
+    static constexpr int Q_TILE = NH * Q_HALF;
+    static constexpr int KV_HALF = TT_KT * 128;
+    static constexpr int SLOT = NH * KV_HALF;
+    static constexpr int OFF_SLOTS = 2 * Q_TILE;
+    static constexpr int BYTES = OFF_SLOTS + TT_SLOTS * SLOT;
+    // tensor memory columns: S / P of stream w at 128 w, O of stream w behind both
+    static constexpr int O_COL = 2 * TT_KT;
+    static_assert(O_COL + 2 * D <= TT_TMEM_COLS, "tensor memory");
+    static_assert(TREE_WINDOWS_MAX * 8 <= TT_SLOTS * SLOT, "window sums fit the ring");
+};
+
+constexpr uint32_t TT_IDESC_S = umma_idesc_bf16(TT_M, TT_KT, 0, 0);
+
+struct TreeShared {
+    uint64_t full[TT_SLOTS], empty[TT_SLOTS];
+    uint64_t masked[TT_MASKS];     // the tile's token mask is written
+    uint64_t s_full[2];            // S of the stream's step is in tensor memory
+    uint64_t p_full[2];            // its weights are (128 arrivals)
+    uint64_t o_done[2];            // its P.V has finished
+    uint64_t drain;
+    alignas(16) uint32_t mask[TT_MASKS][TT_SEQ_WORDS];
+    uint32_t tmem;
+    int abort_flag;
+};
+
+__device__ __forceinline__ bool tt_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
+    const uint32_t b = smem_u32(bar);
+    if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(b, parity)) {
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > WAIT_LIMIT_NS) {
+            *abort_flag = 1;
+            flag_error(dev_err, PA_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(TT_THREADS, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
+    using Geo = TreeGeom<D>;
+    constexpr int NH = Geo::NH, KS = D / 16;
+    constexpr uint32_t IDESC_O = umma_idesc_bf16(TT_M, D, 0, 1);
+
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    __shared__ TreeShared sh;
+    volatile int* abort_flag = &sh.abort_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        sh.abort_flag = 0;
+        for (int i = 0; i < TT_SLOTS; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < TT_MASKS; ++i) mbar_init(smem_u32(&sh.masked[i]), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.s_full[i]), 1);
+            mbar_init(smem_u32(&sh.p_full[i]), TT_M);
+            mbar_init(smem_u32(&sh.o_done[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        fence_barrier_init();
+        prefetch_tensor_map(&tm_k);
+        prefetch_tensor_map(&tm_v);
+    }
+    if (warp == 0) tmem_alloc(smem_u32(&sh.tmem), TT_TMEM_COLS);
+    pdl_wait();
+    pdl_launch_dependents();
+    TreeWalker<TT_ROWS, TT_KT> walk;
+    tree_begin(a, reinterpret_cast<long long*>(smem + Geo::OFF_SLOTS), walk);
+    fence_proxy_async_smem();   // the window sums lie where copies land next
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const uint32_t sQ = smem_u32(smem), sSlots = smem_u32(smem + Geo::OFF_SLOTS);
+    const int B = a.block_size;
+
+    TreeRun r;
+    if (warp == TT_LOAD_WARP) {
+        // ---- copies ---------------------------------------------------------
+        uint32_t ring = 0, tiles = 0;   // slots and tiles passed so far
+        bool ok = true;
+        const int per = TT_KT / B;      // blocks of a tile: one lane each (at most 16)
+        while (ok && walk.next(a, r)) {
+            if (r.starts && lane == 0) tree_record(a, r);
+            const int32_t* table = a.block_tables + static_cast<size_t>(r.s) * a.max_blocks;
+            auto entry_at = [&](int t) {   // the lane's block-table entry of tile t, -2 past the context
+                const int p = t * TT_KT + lane * B;
+                return t < r.t1 && lane < per && p < r.ctx ? table[p >> a.log2_block] : -2;
+            };
+            int entry = entry_at(r.t0);
+            for (int t = r.t0; t < r.t1 && ok; ++t) {
+                const int next = entry_at(t + 1);
+                const bool bad = entry != -2 && (entry < 0 || entry >= a.num_blocks);
+                const bool here = entry >= 0 && !bad;
+                if (bad) flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
+                const uint32_t bytes = __popc(__ballot_sync(FULL_MASK, here)) * NH * static_cast<uint32_t>(B) * 128u;
+                const int y = here ? (entry * a.num_kv_heads + r.kvh) * B : 0;
+                // tokens of the tile that take part: in the context and in a valid block
+                const int left = r.ctx - t * TT_KT - lane * B;
+                uint32_t part = 0;
+                if (here) part = left >= B ? (B == 32 ? 0xffffffffu : (1u << B) - 1u) : (1u << left) - 1u;
+                const int lanes_per_word = 32 / B;
+                part <<= (lane % lanes_per_word) * B;
+                for (int o = 1; o < lanes_per_word; o <<= 1) part |= __shfl_xor_sync(FULL_MASK, part, o);
+                // K, then V; the token mask goes with K.  Its ring entry is free:
+                // the slot of K was last used two tiles and a half ago, by a tile
+                // whose step (and those before it) has been through softmax.
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const uint32_t slot = ring % TT_SLOTS;
+                    bool w = true;
+                    if (ring >= TT_SLOTS)
+                        w = tt_wait(&sh.empty[slot], ((ring / TT_SLOTS) - 1) & 1u, abort_flag, a.dev_err);
+                    if (!__all_sync(FULL_MASK, w)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&sh.full[slot]);
+                    if (v == 0) {
+                        if (lane < per && lane % lanes_per_word == 0) sh.mask[tiles % TT_MASKS][lane / lanes_per_word] = part;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sh.masked[tiles % TT_MASKS]));
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (here) {
+                        const uint32_t dst = sSlots + slot * Geo::SLOT + lane * B * 128;
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) tma_load_2d(dst + h * Geo::KV_HALF, v == 0 ? &tm_k : &tm_v, bar, 64 * h, y);
+                    }
+                    ++ring;
+                }
+                ++tiles;
+                entry = next;
+            }
+        }
+        // after a timeout: the latest copy into every slot must have landed
+        if (*abort_flag && lane == 0) {
+            const uint32_t n = ring < TT_SLOTS ? ring : TT_SLOTS;
+            for (uint32_t k = 1; k <= n; ++k) {
+                const uint32_t g = ring - k;
+                mbar_wait_bounded(smem_u32(&sh.full[g % TT_SLOTS]), (g / TT_SLOTS) & 1u, DRAIN_LIMIT_NS);
+            }
+        }
+    } else if (warp == TT_MMA_WARP) {
+        // ---- MMAs -----------------------------------------------------------
+        uint32_t ring = 0;        // ring position of the run's first K tile
+        uint32_t uses[2] = {0, 0};   // steps of each stream so far
+        while (walk.next(a, r)) {
+            named_barrier_sync(TT_Q_BARRIER, TT_SOFTMAX + 32);   // Q written, O of the last run read
+            const bool two = r.rows > TT_M;      // two row tiles: every tile is two steps
+            const int nt = r.t1 - r.t0, steps = two ? 2 * nt : nt;
+            if (lane == 0 && !*abort_flag) {
+                tmem_fence_after_sync();
+                auto k_at = [&](int i) { return ring + 2u * (two ? i >> 1 : i); };   // ring position of step i's K
+                auto mma_s = [&](int i) {
+                    const int w = i & 1;
+                    const uint32_t slot = k_at(i) % TT_SLOTS;
+                    const uint32_t q = sQ + (two && w ? Geo::Q_TILE : 0), k = sSlots + slot * Geo::SLOT;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const uint32_t off = (ks % 4) * 32;   // k-step inside a 128-byte row
+                        umma_bf16(tmem + TT_KT * w, umma_desc_sw128(q + (ks / 4) * Geo::Q_HALF + off, 16, 1024),
+                                  umma_desc_sw128(k + (ks / 4) * Geo::KV_HALF + off, 16, 1024), TT_IDESC_S, ks > 0 ? 1u : 0u);
+                    }
+                    umma_commit(smem_u32(&sh.s_full[w]));
+                    if (!two || w == 1) umma_commit(smem_u32(&sh.empty[slot]));   // K's last reader
+                };
+                auto mma_o = [&](int i) {
+                    const int w = i & 1;
+                    const uint32_t slot = (k_at(i) + 1) % TT_SLOTS, v = sSlots + slot * Geo::SLOT;
+#pragma unroll
+                    for (int kk = 0; kk < TT_KT / 16; ++kk) {
+                        const uint64_t bd = umma_desc_sw128(v + kk * 2048, Geo::KV_HALF, 1024);
+                        const uint32_t p = tmem + TT_KT * w + 32 * (kk / 2) + 8 * (kk % 2);
+                        umma_bf16_tmem_a(tmem + Geo::O_COL + D * w, p, bd, IDESC_O, (i >= 2 || kk > 0) ? 1u : 0u);
+                        umma_bf16_tmem_a(tmem + Geo::O_COL + D * w, p + 16, bd, IDESC_O, 1u);
+                    }
+                    if (!two || w == 1) umma_commit(smem_u32(&sh.empty[slot]));
+                    umma_commit(smem_u32(&sh.o_done[w]));
+                };
+                auto landed = [&](uint32_t g) { return mbar_test_wait(smem_u32(&sh.full[g % TT_SLOTS]), (g / TT_SLOTS) & 1u); };
+                // S(i) needs its K and P.V(i - 2) done with the stream's buffer;
+                // P.V(i) needs its weights and its V.  Each goes in order; the
+                // barriers are tested without blocking.
+                int ns = 0, no = 0;
+                uint64_t t_last = global_timer_ns();
+                while (no < steps) {
+                    bool progressed = false;
+                    // uses[w]: the stream's P.V issued so far, the last of them step ns - 2
+                    if (ns < steps && landed(k_at(ns)) &&
+                        (ns < 2 || (no > ns - 2 && mbar_test_wait(smem_u32(&sh.o_done[ns & 1]), (uses[ns & 1] - 1) & 1u)))) {
+                        tmem_fence_after_sync();
+                        mma_s(ns++);
+                        progressed = true;
+                    }
+                    if (no < ns && mbar_test_wait(smem_u32(&sh.p_full[no & 1]), uses[no & 1] & 1u) && landed(k_at(no) + 1)) {
+                        tmem_fence_after_sync();
+                        mma_o(no);
+                        ++uses[no & 1];
+                        ++no;
+                        progressed = true;
+                    }
+                    if (progressed) {
+                        t_last = global_timer_ns();
+                    } else if (*abort_flag) {
+                        break;
+                    } else if (global_timer_ns() - t_last > WAIT_LIMIT_NS) {
+                        *abort_flag = 1;
+                        flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+                        break;
+                    }
+                }
+            }
+            __syncwarp();
+            ring += 2 * nt;
+        }
+        if (*abort_flag && lane == 0) {   // every MMA issued so far
+            umma_commit(smem_u32(&sh.drain));
+            mbar_wait_bounded(smem_u32(&sh.drain), 0, DRAIN_LIMIT_NS);
+        }
+    } else {
+        // ---- softmax --------------------------------------------------------
+        const int w = warp >> 2;                  // stream
+        const int row = tid & (TT_M - 1);         // row of the stream's tile = tensor memory lane
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t s_col = lanes + TT_KT * w, o_col = lanes + Geo::O_COL + D * w;
+        // a zero scale would turn the masked -inf into NaN: the smallest normal
+        // numbers leave every weight of a row at 1 just as well
+        const float sl2 = a.scale_log2 == 0.f ? 1e-37f : a.scale_log2;
+        uint32_t ring = 0, tiles = 0, use = 0;    // ring position and tile of the run's start; the stream's steps
+        while (walk.next(a, r)) {
+            const bool two = r.rows > TT_M;
+            const int nt = r.t1 - r.t0;
+            // Q: one or two tiles of 128 rows; rows past the unit's are zero
+            {
+                constexpr int CH = D / 8;         // 16-byte chunks of a row
+                const int chunks = (two ? 2 : 1) * TT_M * CH;
+                constexpr int BATCH = 8;
+                for (int i0 = tid; i0 < chunks; i0 += BATCH * TT_SOFTMAX) {
+                    uint4 v[BATCH];
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int i = i0 + k * TT_SOFTMAX, rr = i / CH;
+                        v[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (i < chunks && rr < r.rows)
+                            v[k] = __ldg(reinterpret_cast<const uint4*>(
+                                       static_cast<const __nv_bfloat16*>(a.q) +
+                                       tree_out_row(a, r.first, r.kvh, r.row0 + rr) * D) + i % CH);
+                    }
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int i = i0 + k * TT_SOFTMAX, rr = i / CH, ch = i % CH;
+                        if (i < chunks)
+                            *reinterpret_cast<uint4*>(smem + (rr / TT_M) * Geo::Q_TILE + (ch / 8) * Geo::Q_HALF +
+                                                      (rr % TT_M) * 128 + (((ch % 8) ^ (rr & 7)) << 4)) = v[k];
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            tmem_fence_before_sync();   // the last run's O was read
+            named_barrier_sync(TT_Q_BARRIER, TT_SOFTMAX + 32);
+
+            const int R = (two ? w * TT_M : 0) + row;       // row of the unit
+            const bool valid = R < r.rows;
+            const bool busy = R - (row & 31) < r.rows;      // the warp has a valid row
+            const int node = valid ? (r.row0 + R) / a.group : 0;
+            const uint32_t* mrow = a.tree_mask + static_cast<size_t>(r.first + node) * a.mask_words32;
+            const int pre = r.ctx - r.n;
+            float m = NEG_INF, l = 0.f;
+            bool ok = __all_sync(FULL_MASK, !*abort_flag);
+            const int step = two ? 1 : 2;
+            int taken = 0;                                  // tiles of the run this stream took
+            for (int j = two ? 0 : w; j < nt && ok; j += step, ++taken) {
+                const uint32_t mi = (tiles + j) % TT_MASKS;
+                const uint32_t vg = ring + 2 * j + 1, vslot = vg % TT_SLOTS;
+                bool ready = tt_wait(&sh.masked[mi], ((tiles + j) / TT_MASKS) & 1u, abort_flag, a.dev_err);
+                const uint4 in = *reinterpret_cast<const uint4*>(sh.mask[mi]);
+                ready = ready && tt_wait(&sh.s_full[w], use & 1u, abort_flag, a.dev_err);
+                const uint32_t inw[4] = {in.x, in.y, in.z, in.w};
+                const bool all_in = (in.x & in.y & in.z & in.w) == 0xffffffffu;
+                if (!all_in) ready = ready && tt_wait(&sh.full[vslot], (vg / TT_SLOTS) & 1u, abort_flag, a.dev_err);
+                if (!__all_sync(FULL_MASK, ready)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after_sync();
+                const int p0 = (r.t0 + j) * TT_KT;
+                if (busy) {
+                    // S is read twice, 32 columns at a time and the next 32 under way:
+                    // for the maximum, then for the weights (128 cycles more of tensor
+                    // memory reads, 64 registers instead of 128)
+                    uint32_t buf[2][32];
+                    const bool every = all_in && p0 + TT_KT <= pre;   // every token seen by every row
+                    float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+                    tmem_issue32(s_col, buf[0]);
+#pragma unroll
+                    for (int c = 0; c < TT_SEQ_WORDS; ++c) {
+                        uint32_t(&x)[32] = buf[c & 1];
+                        tmem_await32(x);
+                        if (c + 1 < TT_SEQ_WORDS) tmem_issue32(s_col + 32 * (c + 1), buf[(c + 1) & 1]);
+                        if (every) {
+                            // the largest x * sl2: the largest x, or the smallest under a negative scale
+                            if (sl2 >= 0.f) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[k]));
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], -__uint_as_float(x[k]));
+                            }
+                        } else {
+                            const uint32_t seen = inw[c] & tree_bits(mrow, a.mask_words32, p0 + 32 * c - pre);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if ((seen >> k) & 1u) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[k]) * sl2);
+                        }
+                    }
+                    float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    if (every) mx *= fabsf(sl2);
+                    const bool up = mx > m + RESCALE_THRESHOLD;
+                    float alpha = 1.f;
+                    if (up) {
+                        alpha = exp2_approx(m - mx);
+                        m = mx;
+                        l *= alpha;
+                    }
+                    const float base = m == NEG_INF ? 0.f : m;
+                    const float unseen = sl2 >= 0.f ? NEG_INF : INFINITY;   // times the scale: -inf
+                    // O may be rescaled only between this stream's P.V steps
+                    if (taken > 0 && __any_sync(FULL_MASK, up)) {
+                        const bool done = tt_wait(&sh.o_done[w], (use - 1) & 1u, abort_flag, a.dev_err);
+                        if (__all_sync(FULL_MASK, done)) {
+                            tmem_fence_after_sync();
+#pragma unroll 1
+                            for (int c0 = 0; c0 < D; c0 += 32) {
+                                float o[32];
+                                tmem_load32(o_col + c0, o);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                                tmem_store32(o_col + c0, o);
+                            }
+                        } else {
+                            ok = false;
+                        }
+                    }
+                    // weights over S, 32 tokens at a time: 16 columns of hi = bf16(p),
+                    // then 16 of lo = bf16(p - hi)
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    tmem_issue32(s_col, buf[0]);
+#pragma unroll
+                    for (int c = 0; c < TT_SEQ_WORDS; ++c) {
+                        uint32_t(&x)[32] = buf[c & 1];
+                        tmem_await32(x);
+                        if (c + 1 < TT_SEQ_WORDS) tmem_issue32(s_col + 32 * (c + 1), buf[(c + 1) & 1]);
+                        if (!every) {
+                            const uint32_t seen = inw[c] & tree_bits(mrow, a.mask_words32, p0 + 32 * c - pre);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((seen >> k) & 1u)) x[k] = __float_as_uint(unseen);
+                        }
+                        uint32_t pw[32];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float p = exp2_approx(fmaf(__uint_as_float(x[2 * k]), sl2, -base));
+                            const float q = exp2_approx(fmaf(__uint_as_float(x[2 * k + 1]), sl2, -base));
+                            sum[k & 3] += p + q;
+                            pw[k] = pack_bf16(p, q);
+                            pw[16 + k] = pack_bf16(p - bf16_lo(pw[k]), q - bf16_hi(pw[k]));
+                        }
+                        tmem_store32_bits(s_col + 32 * c, pw);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                }
+                // value rows of tokens that take no part may hold anything, NaN
+                // too: zero them, so that 0 * V stays 0 (two row tiles share the
+                // slot: stream 0's P.V comes first, and its warps do it)
+                if (!all_in && (!two || w == 0)) {
+                    uint8_t* vs = smem + Geo::OFF_SLOTS + vslot * Geo::SLOT;
+                    for (int i = row; i < TT_KT * NH * 8; i += TT_M) {
+                        const int tok = i / (NH * 8), ch = i % (NH * 8);
+                        if (!((inw[tok >> 5] >> (tok & 31)) & 1u))
+                            *reinterpret_cast<uint4*>(vs + (ch / 8) * Geo::KV_HALF + tok * 128 + (ch % 8) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_fence_before_sync();
+                mbar_arrive(smem_u32(&sh.p_full[w]));
+                ++use;
+            }
+            // the run's last P.V of this stream
+            if (ok && taken > 0) ok = tt_wait(&sh.o_done[w], (use - 1) & 1u, abort_flag, a.dev_err);
+            tmem_fence_after_sync();
+
+            // epilogue.  Two row tiles: every stream stores its own rows.  One:
+            // both streams hold a part of the same rows; each stores half of the
+            // columns of both parts together.
+            float M = m, L = l, c0 = 1.f, c1 = 0.f;
+            if (!two) {
+                float2* ml = reinterpret_cast<float2*>(smem + Geo::Q_TILE);   // the row tile that is not in use
+                ml[w * TT_M + row] = make_float2(m, l);
+                tmem_fence_before_sync();
+                named_barrier_sync(TT_ML_BARRIER, TT_SOFTMAX);
+                tmem_fence_after_sync();
+                const float2 x0 = ml[row], x1 = ml[TT_M + row];
+                M = fmaxf(x0.x, x1.x);
+                c0 = M == NEG_INF ? 0.f : exp2_approx(x0.x - M);
+                c1 = M == NEG_INF ? 0.f : exp2_approx(x1.x - M);
+                L = c0 * x0.y + c1 * x1.y;
+            }
+            const bool go = __all_sync(FULL_MASK, ok && !*abort_flag);
+            if (go && busy) {
+                const bool whole = r.t0 == 0 && r.t1 == r.nt;
+                const bool both = !two && nt > 1;
+                const int slot = 2 * blockIdx.x + (r.starts ? 0 : 1);
+                const int col0 = two ? 0 : w * (D / 2), cols = two ? D : D / 2;
+                const uint32_t first = lanes + Geo::O_COL + (two ? D * w : 0);
+                const float inv = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+                // a row that has seen nothing: its O is zero whatever the buffer holds
+                const float f0 = c0 * inv, f1 = c1 * inv;
+                const size_t at = valid ? tree_out_row(a, r.first, r.kvh, r.row0 + R) * D : 0;
+                float4* acc = reinterpret_cast<float4*>(tree_part(a, slot, D)) + R;
+#pragma unroll 1
+                for (int c = col0; c < col0 + cols; c += 32) {
+                    float o[32];
+                    tmem_load32(first + c, o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] *= f0;
+                    if (both) {
+                        float o1[32];
+                        tmem_load32(first + D + c, o1);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = fmaf(o1[k], f1, o[k]);
+                    }
+                    if (valid && !whole) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            acc[(c / 4 + k) * a.part_rows] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    } else if (valid && a.out_f32) {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    } else if (valid) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at + c);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                                                pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+                    }
+                    __syncwarp();
+                }
+                if (valid && !whole && (two || w == 0)) a.part_ml[static_cast<size_t>(slot) * a.part_rows + R] = make_float2(M, L);
+            }
+            ring += 2 * nt;
+            tiles += nt;
+        }
+    }
+
+    __syncwarp();
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    if (warp == 0) tmem_free(tmem, TT_TMEM_COLS);
+}
+
+template <int D>
+int launch(const TreeArgs& a, int ctas, cudaStream_t st) {
+    static KernelSlot slot;
+    CUtensorMap tk, tv;
+    if (!encode_pool_map(&tk, a.k_cache, a.num_blocks, a.num_kv_heads, a.block_size, D, a.block_size) ||
+        !encode_pool_map(&tv, a.v_cache, a.num_blocks, a.num_kv_heads, a.block_size, D, a.block_size))
+        return PA_ERR_CUDA;
+    const int smem = TreeGeom<D>::BYTES + 1024;
+    auto kern = tree_tc_kernel<D>;
+    if (prepare_kernel(slot, reinterpret_cast<const void*>(kern), TT_THREADS, smem) <= 0) return PA_ERR_CUDA;
+    return launch_status(launch_pdl(kern, dim3(ctas), dim3(TT_THREADS), smem, st, tk, tv, a));
+}
+
+}  // namespace
+
+bool tree_tc_eligible(pa_dtype dtype, int block_size) {
+    return dtype == PA_BF16 && (block_size == 8 || block_size == 16 || block_size == 32);
+}
+
+int tree_tc_rows() { return TT_ROWS; }
+
+int launch_tree_tc(const TreeArgs& a, int head_dim, int ctas, cudaStream_t st) {
+    return head_dim == 128 ? launch<128>(a, ctas, st) : launch<64>(a, ctas, st);
+}
+
+}  // namespace pa

@@ -43,6 +43,11 @@ SIGNATURES = {
                         _i, _vp, _sz, _i, _i32p, _vp]),
     "pa_decode_noalloc": (_i, [_vp, _i, _vp, _vp, _vp, _i32p, _i32p, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                _i, _i, _i32p, _vp]),
+    "pa_tree_workspace_bytes": (_sz, [_i, _i, _i]),
+    "pa_tree_uses_tensor_cores": (_i, [_i, _i]),
+    "pa_tree_decode": (_i, [_vp, _i, _vp, _vp, _vp, _i32p, _i32p, _i32p, _i64p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                            _f, _vp, _sz, _i, _i32p, _vp]),
+    "pa_tree_mask": (_i, [_vp, _i, _i, _vp]),
     "pa_decode_weights_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "pa_decode_weights": (_i, [_vp, _i, _vp, _vp, _i32p, _i, _vp, _vp, _vp, _i32p, _i32p, _i, _i, _i, _i, _i, _i, _i,
                                _i, _f, _i, _vp, _sz, _i, _i32p, _vp]),
@@ -294,6 +299,65 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_dst_pairs: tor
                             _dev(src_dst_pairs, "src_dst_pairs", torch.int64), n, block_bytes,
                             k_cache.shape[0], _opt_err(dev_err), _stream_handle(stream))
     _check(rc, "pa_copy_blocks")
+
+
+TREE_MAX_WORDS = 8
+
+
+def alloc_tree_workspace(num_tokens: int, num_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """Workspace of ``tree_decode`` for up to ``num_tokens`` drafted tokens."""
+    n = lib.pa_tree_workspace_bytes(num_tokens, num_heads, head_dim)
+    if n == 0:
+        raise ValueError("invalid arguments for pa_tree_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def tree_uses_tensor_cores(dtype: torch.dtype, block_size: int) -> bool:
+    """Whether ``tree_decode`` serves such a pool on the tensor cores (tcgen05)."""
+    return bool(lib.pa_tree_uses_tensor_cores(dtype_code(dtype), block_size))
+
+
+def tree_mask(parents, mask_words: Optional[int] = None) -> torch.Tensor:
+    """Mask rows of one tree (int64 [n][mask_words], host): parents[i] is node i's parent, a node
+    before it, or negative where it follows the prefix."""
+    import numpy as np
+
+    p = np.ascontiguousarray(parents, dtype=np.int32)
+    words = max(1, -(-len(p) // 64)) if mask_words is None else int(mask_words)
+    mask = np.zeros((len(p), max(words, 1)), dtype=np.int64)
+    _check(lib.pa_tree_mask(p.ctypes.data, len(p), words, mask.ctypes.data), "pa_tree_mask")
+    return torch.from_numpy(mask)
+
+
+def tree_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                mask: torch.Tensor, scale: float, *, max_context_len: int = 0,
+                workspace: Optional[torch.Tensor] = None, dev_err: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of drafted tokens q [T][Hq][d] (sequence s owns rows query_start[s] ..
+    query_start[s+1]-1) against the paged context: each sees its sequence's prefix and the nodes its
+    ``mask`` row (int64 [T][words], see ``tree_mask``) names.  Writes and returns ``out``."""
+    NB, Hkv, B, d = k_cache.shape
+    T, Hq, dq = q.shape
+    S = context_lens.shape[0]
+    if dq != d or v_cache.shape != k_cache.shape or out.shape != q.shape or tuple(query_start.shape) != (S + 1,):
+        raise ValueError("q/out must be [num_tokens][num_heads][head_dim], query_start [num_seqs + 1]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [num_seqs][max_blocks]")
+    if mask.dim() != 2 or mask.shape[0] != T:
+        raise ValueError("mask must be [num_tokens][words]")
+    dt = k_cache.dtype
+    if workspace is None:
+        workspace = alloc_tree_workspace(T, Hq, d, q.device)
+    rc = lib.pa_tree_decode(
+        _dev(out, "out"), dtype_code(out.dtype), _dev(q, "q", dt), _dev(k_cache, "k_cache", dt),
+        _dev(v_cache, "v_cache", dt), _dev(block_tables, "block_tables", torch.int32),
+        _dev(context_lens, "context_lens", torch.int32), _dev(query_start, "query_start", torch.int32),
+        _dev(mask, "mask", torch.int64), mask.shape[1], S, T, Hq, Hkv, d, B, NB, block_tables.shape[1],
+        max_context_len, float(scale), _dev(workspace, "workspace", torch.uint8), workspace.numel(), dtype_code(dt),
+        _opt_err(dev_err), _stream_handle(stream))
+    _check(rc, "pa_tree_decode")
+    return out
 
 
 def alloc_weights_workspace(num_seqs: int, num_heads: int, head_dim: int, capacity: int,

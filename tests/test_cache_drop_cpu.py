@@ -329,3 +329,50 @@ def test_bm_compact_lockstep_with_the_python_manager(pa):
             for x, sq in seqs.items():
                 assert native.block_table(x) == sq.block_table and native.num_tokens(x) == sq.num_tokens
             assert [native.ref_count(b) for b in range(NB)] == pool.ref_cnt.tolist()
+
+
+# ---------------------------------------------------------------------------
+# trees
+# ---------------------------------------------------------------------------
+
+def tree_call(pa, **over):
+    a = dict(out=P, od=0, q=P, k=P, v=P, t=P, c=P, qs=P, m=P, words=1, S=2, T=6, Hq=4, Hkv=2, d=64, B=16, NB=8, mb=8, mc=0,
+             scale=0.1, ws=P, wsb=1 << 30, dt=1, err=None, st=None)
+    a.update(over)
+    return pa.lib.pa_tree_decode(*a.values())
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(T=0, S=0), 0), (dict(S=0), 1), (dict(T=-1), 1), (dict(q=None), 1), (dict(m=None), 1), (dict(m=P + 4), 1),
+    (dict(qs=P + 2), 1), (dict(words=0), 1), (dict(words=9), 2), (dict(d=256), 2), (dict(B=12), 2), (dict(Hq=5), 1),
+    (dict(od=1, dt=0), 2), (dict(ws=None), 1), (dict(ws=P + 16), 1), (dict(wsb=1000), 3), (dict(scale=float("nan")), 1),
+    (dict(NB=1 << 28), 2), (dict(mb=1 << 28), 1), (dict(S=1 << 20), 2), (dict(mc=-1), 1), (dict(dt=2), 1),
+])
+def test_tree_decode_refusals(pa, over, status):
+    assert tree_call(pa, **over) == status
+
+
+def test_tree_workspace_does_not_grow_with_the_batch(pa):
+    f = pa.lib.pa_tree_workspace_bytes
+    assert f(1, 32, 128) < f(8, 32, 128) == f(4096, 32, 128) < 64 << 20
+    assert f(-1, 32, 128) == 0 and f(1, 0, 128) == 0
+
+
+def test_tree_mask_from_parents(pa):
+    m = pa.tree_mask([-1, 0, 0, 1, -1])
+    assert m.tolist() == [[1], [3], [5], [11], [16]]
+    rng = np.random.default_rng(3)
+    parents = [-1] + [int(rng.integers(-1, i)) for i in range(1, 130)]
+    m = pa.tree_mask(parents, 4).numpy().astype(np.uint64)
+    for i in range(130):
+        seen, j = set(), i
+        while j >= 0:
+            seen.add(j)
+            j = parents[j]
+        assert seen == {b for b in range(256) if (int(m[i, b // 64]) >> (b % 64)) & 1}
+    for bad in ([0], [-1, 1], [-1, 2, 0]):
+        with pytest.raises(pa.PagedAttentionError):
+            pa.tree_mask(bad)
+    with pytest.raises(pa.PagedAttentionError):
+        pa.tree_mask([-1] * 65, 1)
+    assert pa.tree_mask([]).shape == (0, 1)

@@ -1,0 +1,177 @@
+"""A model of the tensor-core tree attention kernel's barrier protocol, on the CPU.
+
+The kernel (csrc/tree_tc.cu) runs a loader warp, an MMA-issuing thread and two
+streams of softmax warps per CTA; the loader runs ahead over the CTA's runs, the
+others meet at a named barrier before each run.  As for the prefill kernel's
+model, whose barriers and clock this one uses: every run must complete under
+random timing, and no parity wait may look at a barrier that is two phases on.
+The token masks' ring, which has no "free" barrier of its own, is checked too:
+no mask may be overwritten before the stream that needs it has read it.
+Planted mistakes must be caught: a single mask instead of a ring, and an S issued
+before the P.V that reads the same buffer has finished.
+"""
+
+import random
+
+import pytest
+
+from test_prefill_protocol_model import Barrier, Sim
+
+SLOTS, MASKS = 5, 4
+
+
+class TreeSim(Sim):
+    def __init__(self, seed, masks=MASKS, early_s=False):
+        super().__init__(seed)
+        self.masks, self.early_s = masks, early_s
+        self.full = [Barrier(f"full[{i}]") for i in range(SLOTS)]
+        self.empty = [Barrier(f"empty[{i}]") for i in range(SLOTS)]
+        self.masked = [Barrier(f"masked[{i}]") for i in range(masks)]
+        self.mask = [None] * masks
+        self.s_full = [Barrier(f"s_full[{w}]") for w in range(2)]
+        self.p_full = [Barrier(f"p_full[{w}]") for w in range(2)]
+        self.o_done = [Barrier(f"o_done[{w}]") for w in range(2)]
+        self.reading = [0, 0]     # P.V issued and not finished, per stream
+
+    def finish_pv(self, w):
+        def done():
+            self.reading[w] -= 1
+            self.o_done[w].arrive()
+        at = max(self.mma_free_at, self.now) + 1
+        self.seq += 1
+        self.events.append((at, self.seq, done))
+
+
+def loader(sim, runs):
+    ring = tile = 0
+    for nt, two in runs:
+        for _ in range(nt):
+            for v in range(2):
+                slot = ring % SLOTS
+                if ring >= SLOTS:
+                    while not sim.empty[slot].passed(ring // SLOTS - 1):
+                        yield
+                if v == 0:
+                    sim.mask[tile % sim.masks] = tile
+                    sim.masked[tile % sim.masks].arrive()
+                yield from sim.pause(2)
+                sim.full[slot].arrive(tx=64)
+                sim.copy(sim.full[slot], 64)
+                ring += 1
+            tile += 1
+
+
+def mma(sim, runs):
+    ring, uses = 0, [0, 0]
+    for nt, two in runs:
+        yield "sync"
+        steps = 2 * nt if two else nt
+        ns = no = 0
+        k_at = lambda i: ring + 2 * (i >> 1 if two else i)  # noqa: E731
+        landed = lambda g: sim.full[g % SLOTS].passed(g // SLOTS)  # noqa: E731
+        while no < steps:
+            if ns < steps and landed(k_at(ns)) and \
+                    (ns < 2 or (no > ns - 2 and (sim.early_s or sim.o_done[ns & 1].passed(uses[ns & 1] - 1)))):
+                if sim.reading[ns & 1]:
+                    raise AssertionError("S issued over weights that a P.V still reads")
+                sim.mma(5)
+                sim.commit(sim.s_full[ns & 1])
+                if not two or ns & 1:
+                    sim.commit(sim.empty[k_at(ns) % SLOTS])
+                ns += 1
+            if no < ns and sim.p_full[no & 1].passed(uses[no & 1]) and landed(k_at(no) + 1):
+                sim.mma(10)
+                sim.reading[no & 1] += 1
+                if not two or no & 1:
+                    sim.commit(sim.empty[(k_at(no) + 1) % SLOTS])
+                sim.finish_pv(no & 1)
+                uses[no & 1] += 1
+                no += 1
+            yield
+            yield from sim.pause(2)
+        ring += 2 * nt
+
+
+def softmax(sim, runs, w):
+    ring = tiles = use = 0
+    for nt, two in runs:
+        yield "sync"
+        taken = 0
+        for j in range(0 if two else w, nt, 1 if two else 2):
+            t = tiles + j
+            while not sim.masked[t % sim.masks].passed(t // sim.masks):
+                yield
+            if sim.mask[t % sim.masks] != t:
+                raise AssertionError("a token mask was overwritten before it was read")
+            while not sim.s_full[w].passed(use):
+                yield
+            if sim.rng.random() < 0.3:          # tokens that take no part: V is zeroed
+                g = ring + 2 * j + 1
+                while not sim.full[g % SLOTS].passed(g // SLOTS):
+                    yield
+            if taken and sim.rng.random() < 0.3:   # rescale
+                while not sim.o_done[w].passed(use - 1):
+                    yield
+            yield from sim.pause(8)
+            sim.p_full[w].arrive()
+            use += 1
+            taken += 1
+        if taken:
+            while not sim.o_done[w].passed(use - 1):
+                yield
+        ring += 2 * nt
+        tiles += nt
+
+
+def run(runs, seed, max_steps=200000, **planted):
+    sim = TreeSim(seed, **planted)
+    roles = {"load": loader(sim, runs), "mma": mma(sim, runs), "s0": softmax(sim, runs, 0), "s1": softmax(sim, runs, 1)}
+    at_sync, finished = set(), set()
+    for _ in range(max_steps):
+        if len(finished) == len(roles):
+            return True
+        order = list(roles)
+        sim.rng.shuffle(order)
+        for name in order:
+            if name in finished or name in at_sync:
+                continue
+            for _ in range(sim.rng.randint(1, 3)):
+                try:
+                    got = next(roles[name])
+                except StopIteration:
+                    finished.add(name)
+                    break
+                if got == "sync":
+                    at_sync.add(name)
+                    break
+        if at_sync == {"mma", "s0", "s1"}:       # the loader does not take part
+            at_sync.clear()
+        if sim.events:
+            sim.events.sort(key=lambda e: e[:2])
+            sim.now = sim.events[0][0]
+            while sim.events and sim.events[0][0] <= sim.now:
+                sim.events.pop(0)[2]()
+        else:
+            sim.now += 1
+    return False
+
+
+def random_runs(rng):
+    return [(rng.randint(1, 9), rng.random() < 0.5) for _ in range(rng.randint(1, 6))]
+
+
+def test_protocol_completes_and_no_wait_falls_two_phases_behind():
+    for seed in range(400):
+        assert run(random_runs(random.Random(seed)), seed), f"deadlock, seed {seed}"
+
+
+@pytest.mark.parametrize("planted", [dict(masks=1), dict(early_s=True)])
+def test_planted_mistakes_are_caught(planted):
+    caught = 0
+    for seed in range(300):
+        try:
+            ok = run(random_runs(random.Random(seed)), seed, max_steps=4000, **planted)
+        except AssertionError:
+            ok = False
+        caught += not ok
+    assert caught > 0
