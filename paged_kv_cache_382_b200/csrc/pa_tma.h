@@ -45,4 +45,22 @@ inline bool encode_pool_map(CUtensorMap* m, const void* pool, int num_blocks, in
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same pool as 8-row groups of 64-column parts: one box brings a whole block
+// of one kv head (B a multiple of 8) and lays it out as [8-row group][64-column
+// part][8 rows][64 columns], so that consecutive blocks continue one another with
+// one group stride.
+inline bool encode_block_map(CUtensorMap* m, const void* pool, int num_blocks, int Hkv, int B, int D) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+    const cuuint64_t dims[4] = {64u, 8u, static_cast<cuuint64_t>(D / 64),
+                                static_cast<cuuint64_t>(num_blocks) * Hkv * (B / 8)};
+    const cuuint64_t strides[3] = {row, 128u, 8 * row};
+    const cuuint32_t box[4] = {64u, 8u, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(B / 8)};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pa

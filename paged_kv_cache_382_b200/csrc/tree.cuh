@@ -8,22 +8,32 @@
 //
 // Work line.  A unit is one row block of one (sequence, kv head): up to ROWS
 // query rows (row r = node r / g, head r % g of the group), all of which read
-// the same K/V.  A unit costs ceil(context / KT) K/V tiles, at least one.  The
-// units' tiles in a row (sequence, kv head, row block) form a line of W tiles
-// that the CTAs cut into equal runs: CTA c of G takes tiles [c W / G,
+// the same K/V.  It takes ceil(context / KT) K/V tiles, at least one, and a tile
+// costs one step per HALF rows (a kernel that works through ROWS = 2 HALF rows
+// needs twice the time for more than HALF of them).  The units' steps in a row
+// (sequence, kv head, row block) form a line of W steps that the CTAs cut into
+// equal shares: CTA c of G takes the tiles whose first step lies in [c W / G,
 // (c + 1) W / G).  Ragged contexts and drafts need no other balancing, few rows
 // over a long context are split as finely as there are SMs, and a CTA leaves at
 // most two units unfinished: a partial (max, sum, unnormalised output) for its
 // first run and one for its last, whatever the batch.  A second kernel joins
-// each cut unit's partials in CTA order.  The cuts depend on the whole batch,
-// so a row's rounding may differ in another batch; a batch gives the same bits
-// every time.
+// each cut unit's partials in CTA order.  Shares have at least two steps, so that
+// each holds the start of a tile.  The cuts depend on the whole batch, so a row's
+// rounding may differ in another batch; a batch gives the same bits every time.
 #pragma once
 
 #include "pa_device.cuh"
 #include "pa_host.h"
 
 namespace pa {
+
+// The run a CTA's share starts with, for the join.
+struct TreeRecord {
+    long long begin;             // the unit's first step on the line
+    int first, kvh, row0, rows;  // its rows (see TreeRun)
+    int t0, nt, per_tile;        // the run's first tile, the unit's tiles, steps per tile
+    int pad;
+};
 
 struct TreeArgs {
     void* out;
@@ -35,7 +45,7 @@ struct TreeArgs {
     const int32_t* query_start;
     const uint32_t* tree_mask;   // [num_tokens][mask_words32]
     int32_t* dev_err;
-    int4* recs;                  // [2 * CTA]: the unit each CTA's run starts in
+    TreeRecord* recs;            // [CTA]: the unit each CTA's share starts in
     long long* line;             // W
     float* part_acc;             // [2 * CTA][head_dim / 4][part_rows][4]
     float2* part_ml;             // [2 * CTA][part_rows]
@@ -77,10 +87,15 @@ __device__ __forceinline__ int tree_tiles(int ctx) {
     return ctx > 0 ? (ctx - 1) / KT + 1 : 1;   // an empty context still writes its zero rows
 }
 
-template <int ROWS, int KT>
+// Steps of a sequence's units, and of one kv head's: row blocks of two halves,
+// the last one of one half when that holds its rows.
+template <int HALF>
+__device__ __forceinline__ int tree_halves(const TreeArgs& a, int n) {
+    return (n * a.group + HALF - 1) / HALF;
+}
+template <int HALF, int KT>
 __device__ __forceinline__ long long tree_cost(const TreeArgs& a, const TreeSeq& t) {
-    const long long rows = static_cast<long long>(t.n) * a.group;
-    return (rows + ROWS - 1) / ROWS * a.num_kv_heads * tree_tiles<KT>(t.ctx);
+    return static_cast<long long>(tree_halves<HALF>(a, t.n)) * a.num_kv_heads * tree_tiles<KT>(t.ctx);
 }
 
 // A run of one unit's tiles.
@@ -88,25 +103,27 @@ struct TreeRun {
     int s, first, n, ctx;   // the sequence
     int kvh, row0, rows;    // kv head; the unit's first row and rows within (node, head) rows
     int t0, t1, nt;         // tiles [t0, t1) of the unit's nt
+    int per_tile;           // steps per tile (1 or 2)
+    long long begin;        // the unit's first step on the line
     bool starts;            // the CTA's first run
 };
 
 // Walks the runs of one CTA; every warp that needs them keeps its own walker
 // (lane l holds the window's l-th sequence).
-template <int ROWS, int KT>
+template <int HALF, int HALVES, int KT>
 struct TreeWalker {
-    long long w, w_begin, w_end;   // position on the line, the CTA's share
-    long long base;                // line position of the window's first sequence
-    int seq0;                      // the window's first sequence
+    static_assert(HALVES == 1 || HALVES == 2, "steps per tile");
+    long long w, w_end;     // position on the line, the end of the CTA's share
+    int seq0;               // the window's first sequence
+    bool started;           // a run was given out
     TreeSeq mine;
-    long long start, cost;         // the lane's sequence on the line
+    long long start, cost;  // the lane's sequence on the line
 
     __device__ __forceinline__ void load(const TreeArgs& a, int first_seq, long long at) {
         const int lane = threadIdx.x & 31;
         seq0 = first_seq;
-        base = at;
         mine = tree_seq(a, seq0 + lane, false);
-        cost = tree_cost<ROWS, KT>(a, mine);
+        cost = tree_cost<HALF, KT>(a, mine);
         long long inc = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -118,50 +135,65 @@ struct TreeWalker {
 
     // The next run, or false at the end of the CTA's share.  Called by all lanes.
     __device__ __forceinline__ bool next(const TreeArgs& a, TreeRun& r) {
-        if (w >= w_end) return false;
-        unsigned past;
-        while ((past = __ballot_sync(FULL_MASK, w < start + cost)) == 0u) {
-            if (seq0 + 32 >= a.num_seqs) return false;   // lengths changed under the launch
-            load(a, seq0 + 32, __shfl_sync(FULL_MASK, start + cost, 31));
+        while (w < w_end) {
+            unsigned past;
+            while ((past = __ballot_sync(FULL_MASK, w < start + cost)) == 0u) {
+                if (seq0 + 32 >= a.num_seqs) return false;   // lengths changed under the launch
+                load(a, seq0 + 32, __shfl_sync(FULL_MASK, start + cost, 31));
+            }
+            const int l = __ffs(past) - 1;
+            r.s = seq0 + l;
+            r.first = __shfl_sync(FULL_MASK, mine.first, l);
+            r.n = __shfl_sync(FULL_MASK, mine.n, l);
+            r.ctx = __shfl_sync(FULL_MASK, mine.ctx, l);
+            const long long seq_start = __shfl_sync(FULL_MASK, start, l);
+            r.nt = tree_tiles<KT>(r.ctx);
+            // kv head, then row block: all of HALVES steps per tile but the last
+            const int halves = tree_halves<HALF>(a, r.n);
+            const long long head_steps = static_cast<long long>(halves) * r.nt;
+            long long off = w - seq_start;
+            r.kvh = static_cast<int>(off / head_steps);
+            off -= r.kvh * head_steps;
+            const long long block_steps = static_cast<long long>(HALVES) * r.nt;
+            const int block = static_cast<int>(off / block_steps);
+            off -= block * block_steps;
+            r.per_tile = min(HALVES, halves - HALVES * block);
+            r.row0 = block * HALF * HALVES;
+            r.rows = min(HALF * HALVES, r.n * a.group - r.row0);
+            r.begin = w - off;
+            // tiles whose first step is in the share
+            const long long unit_steps = static_cast<long long>(r.per_tile) * r.nt;
+            const long long end = r.begin + unit_steps < w_end ? unit_steps : w_end - r.begin;
+            r.t0 = static_cast<int>((off + r.per_tile - 1) / r.per_tile);
+            r.t1 = static_cast<int>((end + r.per_tile - 1) / r.per_tile);
+            w = r.begin + end;
+            if (r.t0 >= r.t1) continue;   // only the second step of a tile whose first is another CTA's
+            r.starts = !started;
+            started = true;
+            return true;
         }
-        const int l = __ffs(past) - 1;
-        r.s = seq0 + l;
-        r.first = __shfl_sync(FULL_MASK, mine.first, l);
-        r.n = __shfl_sync(FULL_MASK, mine.n, l);
-        r.ctx = __shfl_sync(FULL_MASK, mine.ctx, l);
-        const long long off = w - __shfl_sync(FULL_MASK, start, l);
-        r.nt = tree_tiles<KT>(r.ctx);
-        const int all = r.n * a.group, blocks = (all + ROWS - 1) / ROWS;
-        const long long unit = off / r.nt;
-        r.kvh = static_cast<int>(unit / blocks);
-        r.row0 = static_cast<int>(unit - static_cast<long long>(r.kvh) * blocks) * ROWS;
-        r.rows = min(ROWS, all - r.row0);
-        r.t0 = static_cast<int>(off - unit * r.nt);
-        const long long left = w_end - w;
-        r.t1 = r.nt - r.t0 <= left ? r.nt : r.t0 + static_cast<int>(left);
-        r.starts = w == w_begin;
-        w += r.t1 - r.t0;
-        return true;
+        return false;
     }
 };
 
-// The CTA's share of the line [lo, hi) for `ctas` CTAs; CTAs past the line's
-// length stay idle, so that no share in between is empty.
-__device__ __forceinline__ long long tree_share(long long W, int ctas, int c) {
-    const long long g = W < ctas ? W : ctas;
-    return c >= g ? W : W / g * c + (W % g) * c / g;
+// CTAs that share a line of W steps, and the first step of CTA c's share.
+__device__ __forceinline__ int tree_sharers(long long W, int ctas) {
+    return W / 2 < ctas ? (W > 1 ? static_cast<int>(W / 2) : 1) : ctas;
+}
+__device__ __forceinline__ long long tree_share(long long W, int sharers, int c) {
+    return c >= sharers ? W : W / sharers * c + (W % sharers) * c / sharers;
 }
 
 // Line length and the CTA's walker.  Called by the whole CTA; `sums` (shared
-// memory, a word per window of 32 sequences and one more) is free again after
-// the caller's next barrier.  CTA 0 reports malformed sequences and keeps the
-// length for the join.
-template <int ROWS, int KT>
-__device__ __forceinline__ void tree_begin(const TreeArgs& a, long long* sums, TreeWalker<ROWS, KT>& walk) {
+// memory, a word per window of 32 sequences) is free again after the caller's
+// next barrier.  CTA 0 reports malformed sequences and keeps the length for the
+// join.
+template <int HALF, int HALVES, int KT>
+__device__ __forceinline__ void tree_begin(const TreeArgs& a, long long* sums, TreeWalker<HALF, HALVES, KT>& walk) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
     const int windows = (a.num_seqs + 31) / 32;
     for (int v = warp; v < windows; v += nwarps) {
-        long long c = tree_cost<ROWS, KT>(a, tree_seq(a, 32 * v + lane, blockIdx.x == 0));
+        long long c = tree_cost<HALF, KT>(a, tree_seq(a, 32 * v + lane, blockIdx.x == 0));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(FULL_MASK, c, o);
         if (lane == 0) sums[v] = c;
@@ -171,9 +203,11 @@ __device__ __forceinline__ void tree_begin(const TreeArgs& a, long long* sums, T
     for (int v = lane; v < windows; v += 32) total += sums[v];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(FULL_MASK, total, o);
-    walk.w_begin = walk.w = tree_share(total, gridDim.x, blockIdx.x);
-    walk.w_end = tree_share(total, gridDim.x, blockIdx.x + 1);
-    // the window that holds the first tile of the share
+    const int sharers = tree_sharers(total, gridDim.x);
+    walk.w = tree_share(total, sharers, blockIdx.x);
+    walk.w_end = tree_share(total, sharers, blockIdx.x + 1);
+    walk.started = false;
+    // the window that holds the first step of the share
     long long at = 0;
     int v = 0;
     while (v + 1 < windows && at + sums[v] <= walk.w) at += sums[v++];
@@ -181,10 +215,8 @@ __device__ __forceinline__ void tree_begin(const TreeArgs& a, long long* sums, T
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.line = total;
 }
 
-// What the join needs of the unit a CTA's share starts in.
 __device__ __forceinline__ void tree_record(const TreeArgs& a, const TreeRun& r) {
-    a.recs[2 * blockIdx.x] = make_int4(r.first, r.kvh, r.row0, r.rows);
-    a.recs[2 * blockIdx.x + 1] = make_int4(r.t0, r.nt, 0, 0);
+    a.recs[blockIdx.x] = TreeRecord{r.begin, r.first, r.kvh, r.row0, r.rows, r.t0, r.nt, r.per_tile, 0};
 }
 
 __device__ __forceinline__ float* tree_part(const TreeArgs& a, int slot, int D) {

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(TS_THREADS) tree_simt_kernel(const TreeArgs a)
     const T* vc = static_cast<const T*>(a.v_cache);
     pdl_wait();
     pdl_launch_dependents();
-    TreeWalker<TS_ROWS, TS_KT> walk;
+    TreeWalker<TS_ROWS, 1, TS_KT> walk;
     tree_begin(a, reinterpret_cast<long long*>(smem_dyn), walk);
     __syncthreads();
 
@@ -261,19 +261,19 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const TreeArgs a,
     pdl_launch_dependents();
     const int c = blockIdx.x + 1;   // share 0 starts no cut
     const long long W = *a.line;
-    const int g = static_cast<int>(W < ctas ? W : ctas);
+    const int g = tree_sharers(W, ctas);
     if (c >= g) return;
-    const int4 r0 = a.recs[2 * c], r1 = a.recs[2 * c + 1];
-    const int t0 = r1.x, nt = r1.y, rows = r0.w;
-    if (t0 == 0) return;                             // the share starts at a unit's start
-    const long long begin = tree_share(W, ctas, c) - t0, end = begin + nt;
-    if (tree_share(W, ctas, c - 1) > begin) return;  // not the unit's first cut
-    const int row0 = blockIdx.y * TJ_ROWS, here = min(TJ_ROWS, rows - row0);
+    const TreeRecord r = a.recs[c];
+    if (r.t0 == 0) return;                               // the share starts with a unit
+    if (tree_share(W, g, c - 1) > r.begin) return;       // not the unit's first cut
+    const int row0 = blockIdx.y * TJ_ROWS, here = min(TJ_ROWS, r.rows - row0);
     if (here <= 0) return;
+    // partials: CTA c - 1's (its first run if its share starts with the unit), then
+    // those of c .. last, which start inside it
     int last = c;
-    while (last + 1 < g && tree_share(W, ctas, last + 1) < end) ++last;
-    // partials: CTA c - 1's (its first run if its share starts with the unit), then those of c .. last
-    const int head = 2 * (c - 1) + (tree_share(W, ctas, c - 1) == begin ? 0 : 1);
+    const long long last_tile = r.begin + static_cast<long long>(r.nt - 1) * r.per_tile;
+    while (last + 1 < g && tree_share(W, g, last + 1) <= last_tile) ++last;
+    const int head = 2 * (c - 1) + (a.recs[c - 1].begin == r.begin ? 0 : 1);
     const int parts = last - c + 2;
     auto slot_of = [&](int p) { return p == 0 ? head : 2 * (c - 1 + p); };
     if (threadIdx.x < here) {
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const TreeArgs a,
             o.z = fmaf(e, v.z, o.z);
             o.w = fmaf(e, v.w, o.w);
         }
-        const size_t at = tree_out_row(a, r0.x, r0.y, r0.z + row0 + rr) * D + 4 * c4;
+        const size_t at = tree_out_row(a, r.first, r.kvh, r.row0 + row0 + rr) * D + 4 * c4;
         if (a.out_f32)
             *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
         else
@@ -330,7 +330,7 @@ inline TreeWs tree_ws(long long num_tokens, int num_heads, int head_dim) {
     w.rows = static_cast<int>(rows < most ? rows : most);
     w.line = 0;
     w.recs = 256;
-    w.ml = w.recs + up256(2 * TREE_CTAS_MAX * sizeof(int4));
+    w.ml = w.recs + up256(TREE_CTAS_MAX * sizeof(TreeRecord));
     w.acc = w.ml + up256(2 * TREE_CTAS_MAX * static_cast<size_t>(w.rows) * sizeof(float2));
     w.total = w.acc + up256(2 * TREE_CTAS_MAX * static_cast<size_t>(w.rows) * head_dim * sizeof(float));
     return w;
@@ -392,7 +392,7 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
     a.dev_err = dev_err;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.line = reinterpret_cast<long long*>(ws + L.line);
-    a.recs = reinterpret_cast<int4*>(ws + L.recs);
+    a.recs = reinterpret_cast<TreeRecord*>(ws + L.recs);
     a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
     a.part_acc = reinterpret_cast<float*>(ws + L.acc);
     a.part_rows = L.rows;

@@ -3,9 +3,9 @@
 // how the work is cut into shares).
 //
 // One CTA per SM takes a share of the work line.  A unit's rows are one or two
-// MMA tiles of 128 rows; K and V come in tiles of 128 tokens.  Two streams,
-// each with its own four softmax warps, S / P buffer and O accumulator in
-// tensor memory, keep the tensor cores and the exponentials busy at once:
+// MMA tiles of 128 rows; K and V come in tiles of 128 tokens.  Two streams, each
+// with its own four softmax warps, S / P buffer and O accumulator in tensor
+// memory, keep the tensor cores and the exponentials busy at once:
 //   more than 128 rows: stream w owns row tile w and takes every K/V tile, so
 //                       K and V are read once for up to 256 rows;
 //   up to 128 rows:     both streams hold the same rows, stream w takes the run's
@@ -16,18 +16,22 @@
 //   O += P . V    (M = 128, N = d, K = 128 tokens; P as a bf16 pair hi + lo,
 //                  written over S: about 16 significant bits, so that the
 //                  weights' rounding stays below the output's)
-// and the MMA thread issues PV(i), S(i + 2) while the other stream's warps
-// work on step i + 1.
+// P is handed over in two halves of 64 tokens, so that P.V of the first runs
+// while the second is computed.  Steps of 64 tokens with two buffers per stream
+// were slower: the tensor cores lose 120 cycles at every change between the two
+// products (1440 cycles a step measured for 900 of MMAs).
 //
 // K and V tiles go through one ring of five 32 KB slots in the order K0 V0 K1
-// V1 ...; a K slot is free again once its S is done, so up to 160 KB are in
-// flight or in use.  The loader warp runs ahead into the CTA's next runs; one
-// lane per block issues that block's bulk copies.
+// V1 ...; a K slot is free again once its S are done, so up to 160 KB are in
+// flight or in use.  Two loader warps, one for K and one for V, run ahead into
+// the CTA's next runs.  One bulk copy brings a whole block.  Next to busy softmax
+// warps a loader needs 2150 cycles for a slot of 8-token blocks (460 alone): one
+// warp for both pools held an SM at 22 GB/s.
 //
 // Per 128-token tile: 64 KB of K and V, 1.5 us at an SM's share of the measured
-// copy bandwidth; per step 512 + 1024 tensor cycles and, on each SM quarter,
-// 1024 cycles of exponentials.  Up to 128 rows one step per tile leaves the
-// kernel bound by HBM; 256 rows take two steps, 1.6 us of MMAs, about the same.
+// copy bandwidth; per step 512 + 1024 tensor cycles and, on each SM quarter, 1024
+// cycles of exponentials.  Up to 128 rows the kernel is bound by HBM; 256 rows
+// take two steps per tile, 1.6 us of MMAs alone.
 //
 // Every wait is bounded: on a timeout the CTA raises PA_DEVERR_TIMEOUT, skips
 // what is left, lets its copies and MMAs drain, frees its tensor memory and
@@ -49,25 +53,28 @@ namespace {
 constexpr int TT_M = 128;               // rows of a stream: the MMA's M
 constexpr int TT_ROWS = 2 * TT_M;       // rows of a unit
 constexpr int TT_KT = 128;              // tokens of a K or V tile
+constexpr int TT_HT = TT_KT / 2;         // tokens of half a step's weights
 constexpr int TT_SLOTS = 5;             // ring slots (one K or V tile each)
 constexpr int TT_MASKS = 4;             // tiles whose token masks are kept
 constexpr int TT_SOFTMAX_WARPS = 8;     // warps 0-3: stream 0, 4-7: stream 1
 constexpr int TT_SOFTMAX = TT_SOFTMAX_WARPS * 32;
 constexpr int TT_MMA_WARP = 8;
-constexpr int TT_LOAD_WARP = 9;
-constexpr int TT_THREADS = (TT_SOFTMAX_WARPS + 2) * 32;
+constexpr int TT_K_WARP = 9;            // copies of K, of V
+constexpr int TT_V_WARP = 10;
+constexpr int TT_THREADS = (TT_SOFTMAX_WARPS + 3) * 32;
 constexpr int TT_TMEM_COLS = 512;
 constexpr int TT_Q_BARRIER = 1;         // Q in shared memory, O read: softmax + MMA warps
 constexpr int TT_ML_BARRIER = 2;        // the streams' (max, sum) exchanged: softmax warps
-constexpr int TT_SEQ_WORDS = TT_KT / 32;
+constexpr int TT_MASK_WORDS = TT_KT / 32;
 
 template <int D>
 struct TreeGeom {
     static constexpr int NH = D / 64;
     static constexpr int Q_HALF = TT_M * 128;          // 128 rows x 64 columns, 128-byte swizzle
     static constexpr int Q_TILE = NH * Q_HALF;
-    static constexpr int KV_HALF = TT_KT * 128;
-    static constexpr int SLOT = NH * KV_HALF;
+    // K and V: 8-row groups of NH 64-column halves, as the copies lay blocks out
+    static constexpr int GROUP = NH * 1024;
+    static constexpr int SLOT = TT_KT / 8 * GROUP;
     static constexpr int OFF_SLOTS = 2 * Q_TILE;
     static constexpr int BYTES = OFF_SLOTS + TT_SLOTS * SLOT;
     // tensor memory columns: S / P of stream w at 128 w, O of stream w behind both
@@ -82,21 +89,33 @@ struct TreeShared {
     uint64_t full[TT_SLOTS], empty[TT_SLOTS];
     uint64_t masked[TT_MASKS];     // the tile's token mask is written
     uint64_t s_full[2];            // S of the stream's step is in tensor memory
-    uint64_t p_full[2];            // its weights are (128 arrivals)
-    uint64_t o_done[2];            // its P.V has finished
+    uint64_t p_full[2][2];         // [stream][half]: its weights are (128 arrivals)
+    uint64_t o_half[2], o_done[2]; // P.V of its first half, of both, has finished
     uint64_t drain;
-    alignas(16) uint32_t mask[TT_MASKS][TT_SEQ_WORDS];
+    alignas(16) uint32_t mask[TT_MASKS][TT_MASK_WORDS];
     uint32_t tmem;
     int abort_flag;
 };
 
+// Bounds a loop of polls: true once WAIT_LIMIT_NS have passed since the first
+// of them.  The global timer is slow to read: only every 256th poll looks.
+struct PollLimit {
+    uint32_t polls = 0;
+    uint64_t t0 = 0;
+    __device__ __forceinline__ bool out() {
+        if (++polls & 255u) return false;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        return t - t0 > WAIT_LIMIT_NS;
+    }
+};
+
 __device__ __forceinline__ bool tt_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
     const uint32_t b = smem_u32(bar);
-    if (mbar_try_wait(b, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+    PollLimit limit;
     while (!mbar_try_wait(b, parity)) {
         if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > WAIT_LIMIT_NS) {
+        if (limit.out()) {
             *abort_flag = 1;
             flag_error(dev_err, PA_DEVERR_TIMEOUT);
             return false;
@@ -127,7 +146,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         for (int i = 0; i < TT_MASKS; ++i) mbar_init(smem_u32(&sh.masked[i]), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.s_full[i]), 1);
-            mbar_init(smem_u32(&sh.p_full[i]), TT_M);
+            mbar_init(smem_u32(&sh.p_full[i][0]), TT_M);
+            mbar_init(smem_u32(&sh.p_full[i][1]), TT_M);
+            mbar_init(smem_u32(&sh.o_half[i]), 1);
             mbar_init(smem_u32(&sh.o_done[i]), 1);
         }
         mbar_init(smem_u32(&sh.drain), 1);
@@ -138,7 +159,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     if (warp == 0) tmem_alloc(smem_u32(&sh.tmem), TT_TMEM_COLS);
     pdl_wait();
     pdl_launch_dependents();
-    TreeWalker<TT_ROWS, TT_KT> walk;
+    TreeWalker<TT_M, 2, TT_KT> walk;
     tree_begin(a, reinterpret_cast<long long*>(smem + Geo::OFF_SLOTS), walk);
     fence_proxy_async_smem();   // the window sums lie where copies land next
     tmem_fence_before_sync();
@@ -149,148 +170,170 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int B = a.block_size;
 
     TreeRun r;
-    if (warp == TT_LOAD_WARP) {
+    if (warp == TT_K_WARP || warp == TT_V_WARP) {
         // ---- copies ---------------------------------------------------------
-        uint32_t ring = 0, tiles = 0;   // slots and tiles passed so far
+        const bool is_v = warp == TT_V_WARP;
+        const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+        uint32_t ring = is_v ? 1 : 0, tiles = 0;   // ring position and tiles passed so far
         bool ok = true;
+        const uint32_t leader = elect_one();
         const int per = TT_KT / B;      // blocks of a tile: one lane each (at most 16)
+        const uint32_t slots = __shfl_sync(FULL_MASK, sSlots, 0);
         while (ok && walk.next(a, r)) {
-            if (r.starts && lane == 0) tree_record(a, r);
+            if (r.starts && !is_v && lane == 0) tree_record(a, r);
             const int32_t* table = a.block_tables + static_cast<size_t>(r.s) * a.max_blocks;
             auto entry_at = [&](int t) {   // the lane's block-table entry of tile t, -2 past the context
                 const int p = t * TT_KT + lane * B;
                 return t < r.t1 && lane < per && p < r.ctx ? table[p >> a.log2_block] : -2;
             };
             int entry = entry_at(r.t0);
-            for (int t = r.t0; t < r.t1 && ok; ++t) {
+            for (int t = r.t0; t < r.t1; ++t) {
                 const int next = entry_at(t + 1);
                 const bool bad = entry != -2 && (entry < 0 || entry >= a.num_blocks);
                 const bool here = entry >= 0 && !bad;
                 if (bad) flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
-                const uint32_t bytes = __popc(__ballot_sync(FULL_MASK, here)) * NH * static_cast<uint32_t>(B) * 128u;
-                const int y = here ? (entry * a.num_kv_heads + r.kvh) * B : 0;
-                // tokens of the tile that take part: in the context and in a valid block
-                const int left = r.ctx - t * TT_KT - lane * B;
-                uint32_t part = 0;
-                if (here) part = left >= B ? (B == 32 ? 0xffffffffu : (1u << B) - 1u) : (1u << left) - 1u;
-                const int lanes_per_word = 32 / B;
-                part <<= (lane % lanes_per_word) * B;
-                for (int o = 1; o < lanes_per_word; o <<= 1) part |= __shfl_xor_sync(FULL_MASK, part, o);
-                // K, then V; the token mask goes with K.  Its ring entry is free:
-                // the slot of K was last used two tiles and a half ago, by a tile
-                // whose step (and those before it) has been through softmax.
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const uint32_t slot = ring % TT_SLOTS;
-                    bool w = true;
-                    if (ring >= TT_SLOTS)
-                        w = tt_wait(&sh.empty[slot], ((ring / TT_SLOTS) - 1) & 1u, abort_flag, a.dev_err);
-                    if (!__all_sync(FULL_MASK, w)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t bar = smem_u32(&sh.full[slot]);
-                    if (v == 0) {
-                        if (lane < per && lane % lanes_per_word == 0) sh.mask[tiles % TT_MASKS][lane / lanes_per_word] = part;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sh.masked[tiles % TT_MASKS]));
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                    __syncwarp();
-                    if (here) {
-                        const uint32_t dst = sSlots + slot * Geo::SLOT + lane * B * 128;
-#pragma unroll
-                        for (int h = 0; h < NH; ++h) tma_load_2d(dst + h * Geo::KV_HALF, v == 0 ? &tm_k : &tm_v, bar, 64 * h, y);
-                    }
-                    ++ring;
+                const uint32_t valid = __ballot_sync(FULL_MASK, here);
+                const uint32_t bytes = __popc(valid) * NH * static_cast<uint32_t>(B) * 128u;
+                const int group = here ? (entry * a.num_kv_heads + r.kvh) * (B / 8) : 0;
+                const uint32_t slot = ring % TT_SLOTS;
+                bool w = true;
+                if (ring >= TT_SLOTS) w = tt_wait(&sh.empty[slot], ((ring / TT_SLOTS) - 1) & 1u, abort_flag, a.dev_err);
+                if (!__all_sync(FULL_MASK, w)) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t bar = smem_u32(&sh.full[slot]);
+                mbar_arrive_expect_tx_elected(leader, bar, bytes);
+                const uint32_t dst = slots + slot * Geo::SLOT;
+                for (int i = 0; i < per; ++i) {
+                    const int at = __shfl_sync(FULL_MASK, group, i);
+                    if ((valid >> i) & 1u)
+                        tma_load_group_elected(leader, dst + i * (B / 8) * Geo::GROUP, map, bar, at);
+                }
+                if (!is_v) {
+                    // tokens of the tile that take part: in the context and in a valid
+                    // block.  The mask's ring entry is free: the slot of K was last
+                    // used two tiles and a half ago, by a tile whose step (and those
+                    // before it) has been through softmax.
+                    const int left = r.ctx - t * TT_KT - lane * B;
+                    uint32_t part = 0;
+                    if (here) part = left >= B ? (B == 32 ? 0xffffffffu : (1u << B) - 1u) : (1u << left) - 1u;
+                    const int lanes_per_word = 32 / B;
+                    part <<= (lane % lanes_per_word) * B;
+                    for (int o = 1; o < lanes_per_word; o <<= 1) part |= __shfl_xor_sync(FULL_MASK, part, o);
+                    if (lane < per && lane % lanes_per_word == 0) sh.mask[tiles % TT_MASKS][lane / lanes_per_word] = part;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.masked[tiles % TT_MASKS]));
+                }
+                ring += 2;
                 ++tiles;
                 entry = next;
             }
         }
         // after a timeout: the latest copy into every slot must have landed
         if (*abort_flag && lane == 0) {
-            const uint32_t n = ring < TT_SLOTS ? ring : TT_SLOTS;
-            for (uint32_t k = 1; k <= n; ++k) {
-                const uint32_t g = ring - k;
-                mbar_wait_bounded(smem_u32(&sh.full[g % TT_SLOTS]), (g / TT_SLOTS) & 1u, DRAIN_LIMIT_NS);
-            }
+            for (uint32_t g = ring; g >= 2 && ring - g < 2 * TT_SLOTS; g -= 2)
+                mbar_wait_bounded(smem_u32(&sh.full[(g - 2) % TT_SLOTS]), ((g - 2) / TT_SLOTS) & 1u, DRAIN_LIMIT_NS);
         }
     } else if (warp == TT_MMA_WARP) {
         // ---- MMAs -----------------------------------------------------------
-        uint32_t ring = 0;        // ring position of the run's first K tile
-        uint32_t uses[2] = {0, 0};   // steps of each stream so far
+        // The whole warp runs this loop and one elected lane issues.
+        const uint32_t leader = elect_one();
+        const uint32_t utmem = __shfl_sync(FULL_MASK, tmem, 0);
+        const uint64_t q_desc = umma_desc_sw128(__shfl_sync(FULL_MASK, sQ, 0), 16, 1024);
+        const uint64_t k_desc = umma_desc_sw128(__shfl_sync(FULL_MASK, sSlots, 0), 16, Geo::GROUP);
+        const uint64_t v_desc = umma_desc_sw128(__shfl_sync(FULL_MASK, sSlots, 0), 1024, Geo::GROUP);
+        const uint32_t bars = __shfl_sync(FULL_MASK, smem_u32(&sh), 0);
+        auto bar_at = [&](const uint64_t* first, uint32_t i) {
+            return bars + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(first) - reinterpret_cast<const uint8_t*>(&sh)) + 8u * i;
+        };
+        auto passed = [&](uint32_t bar, uint32_t parity) { return __all_sync(FULL_MASK, mbar_test_wait(bar, parity)); };
+        uint32_t base[2] = {0, 0};            // steps of each stream in earlier runs
+        uint32_t k_slot = 0, k_phase = 0;     // ring slot of the next S's K and its phase
+        uint32_t v_slot = 1, v_phase = 0;     // of the next P.V's V
+        auto advance = [](uint32_t& slot, uint32_t& phase) {
+            slot += 2;
+            if (slot >= TT_SLOTS) {
+                slot -= TT_SLOTS;
+                phase ^= 1u;
+            }
+        };
         while (walk.next(a, r)) {
             named_barrier_sync(TT_Q_BARRIER, TT_SOFTMAX + 32);   // Q written, O of the last run read
-            const bool two = r.rows > TT_M;      // two row tiles: every tile is two steps
-            const int nt = r.t1 - r.t0, steps = two ? 2 * nt : nt;
-            if (lane == 0 && !*abort_flag) {
-                tmem_fence_after_sync();
-                auto k_at = [&](int i) { return ring + 2u * (two ? i >> 1 : i); };   // ring position of step i's K
-                auto mma_s = [&](int i) {
-                    const int w = i & 1;
-                    const uint32_t slot = k_at(i) % TT_SLOTS;
-                    const uint32_t q = sQ + (two && w ? Geo::Q_TILE : 0), k = sSlots + slot * Geo::SLOT;
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const uint32_t off = (ks % 4) * 32;   // k-step inside a 128-byte row
-                        umma_bf16(tmem + TT_KT * w, umma_desc_sw128(q + (ks / 4) * Geo::Q_HALF + off, 16, 1024),
-                                  umma_desc_sw128(k + (ks / 4) * Geo::KV_HALF + off, 16, 1024), TT_IDESC_S, ks > 0 ? 1u : 0u);
-                    }
-                    umma_commit(smem_u32(&sh.s_full[w]));
-                    if (!two || w == 1) umma_commit(smem_u32(&sh.empty[slot]));   // K's last reader
-                };
-                auto mma_o = [&](int i) {
-                    const int w = i & 1;
-                    const uint32_t slot = (k_at(i) + 1) % TT_SLOTS, v = sSlots + slot * Geo::SLOT;
-#pragma unroll
-                    for (int kk = 0; kk < TT_KT / 16; ++kk) {
-                        const uint64_t bd = umma_desc_sw128(v + kk * 2048, Geo::KV_HALF, 1024);
-                        const uint32_t p = tmem + TT_KT * w + 32 * (kk / 2) + 8 * (kk % 2);
-                        umma_bf16_tmem_a(tmem + Geo::O_COL + D * w, p, bd, IDESC_O, (i >= 2 || kk > 0) ? 1u : 0u);
-                        umma_bf16_tmem_a(tmem + Geo::O_COL + D * w, p + 16, bd, IDESC_O, 1u);
-                    }
-                    if (!two || w == 1) umma_commit(smem_u32(&sh.empty[slot]));
-                    umma_commit(smem_u32(&sh.o_done[w]));
-                };
-                auto landed = [&](uint32_t g) { return mbar_test_wait(smem_u32(&sh.full[g % TT_SLOTS]), (g / TT_SLOTS) & 1u); };
-                // S(i) needs its K and P.V(i - 2) done with the stream's buffer;
-                // P.V(i) needs its weights and its V.  Each goes in order; the
-                // barriers are tested without blocking.
-                int ns = 0, no = 0;
-                uint64_t t_last = global_timer_ns();
-                while (no < steps) {
-                    bool progressed = false;
-                    // uses[w]: the stream's P.V issued so far, the last of them step ns - 2
-                    if (ns < steps && landed(k_at(ns)) &&
-                        (ns < 2 || (no > ns - 2 && mbar_test_wait(smem_u32(&sh.o_done[ns & 1]), (uses[ns & 1] - 1) & 1u)))) {
+            const bool two = __shfl_sync(FULL_MASK, r.per_tile, 0) == 2;   // every tile is a step of both streams
+            const int nt = __shfl_sync(FULL_MASK, r.t1 - r.t0, 0);
+            const int steps = two ? 2 * nt : nt;
+            if (__any_sync(FULL_MASK, *abort_flag)) continue;
+            tmem_fence_after_sync();
+            // Step i of the run: stream i % 2, its step base + i / 2.  S(i) needs its K
+            // and P.V(i - 2) done with the buffer; half h of P.V(i) needs its weights
+            // and its V.  Each goes in order; the barriers are tested without blocking.
+            int ns = 0, no = 0, h = 0;
+            PollLimit limit;
+            while (no < steps) {
+                bool progressed = false;
+                if (ns < steps && ns < no + 2 && passed(bar_at(sh.full, k_slot), k_phase)) {
+                    const uint32_t w = ns & 1, use = (w ? base[1] : base[0]) + (ns >> 1);
+                    if (ns < 2 || passed(bar_at(sh.o_done, w), (use & 1u) ^ 1u)) {
                         tmem_fence_after_sync();
-                        mma_s(ns++);
+                        const uint64_t qd = q_desc + (two && w ? Geo::Q_TILE >> 4 : 0);
+                        const uint64_t kd = k_desc + ((k_slot * Geo::SLOT) >> 4);
+                        const bool free_k = !two || w == 1;   // K's last reader
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) {
+                            // k-step inside a 128-byte row, 64-column half
+                            constexpr int STEP = 32 >> 4;
+                            umma_bf16_elected(leader, utmem + TT_KT * w,
+                                              qd + (ks % 4) * STEP + (ks / 4) * (Geo::Q_HALF >> 4),
+                                              kd + (ks % 4) * STEP + (ks / 4) * (1024 >> 4), TT_IDESC_S,
+                                              ks > 0 ? 1u : 0u);
+                        }
+                        umma_commit_elected(leader, bar_at(sh.s_full, w));
+                        if (free_k) umma_commit_elected(leader, bar_at(sh.empty, k_slot));
+                        if (free_k) advance(k_slot, k_phase);
+                        ++ns;
                         progressed = true;
-                    }
-                    if (no < ns && mbar_test_wait(smem_u32(&sh.p_full[no & 1]), uses[no & 1] & 1u) && landed(k_at(no) + 1)) {
-                        tmem_fence_after_sync();
-                        mma_o(no);
-                        ++uses[no & 1];
-                        ++no;
-                        progressed = true;
-                    }
-                    if (progressed) {
-                        t_last = global_timer_ns();
-                    } else if (*abort_flag) {
-                        break;
-                    } else if (global_timer_ns() - t_last > WAIT_LIMIT_NS) {
-                        *abort_flag = 1;
-                        flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
-                        break;
                     }
                 }
+                if (no < ns) {
+                    const uint32_t w = no & 1, use = (w ? base[1] : base[0]) + (no >> 1);
+                    if (passed(bar_at(&sh.p_full[0][0], 2 * w + h), use & 1u) &&
+                        (h == 1 || passed(bar_at(sh.full, v_slot), v_phase))) {
+                        tmem_fence_after_sync();
+                        const uint64_t vd = v_desc + ((v_slot * Geo::SLOT + h * (Geo::SLOT / 2)) >> 4);
+                        const uint32_t p_tmem = utmem + TT_KT * w + TT_HT * h;
+                        const uint32_t o_tmem = utmem + Geo::O_COL + D * w;
+                        const uint32_t more = no >= 2 || h == 1 ? 1u : 0u;   // 0: the stream's first P.V of the run
+                        const bool free_v = h == 1 && (!two || w == 1);
+#pragma unroll
+                        for (int kk = 0; kk < TT_HT / 16; ++kk) {
+                            const uint32_t p = p_tmem + 32 * (kk / 2) + 8 * (kk % 2);
+                            umma_bf16_tmem_a_elected(leader, o_tmem, p, vd + kk * (2 * Geo::GROUP >> 4), IDESC_O, kk > 0 ? 1u : more);
+                            umma_bf16_tmem_a_elected(leader, o_tmem, p + 16, vd + kk * (2 * Geo::GROUP >> 4), IDESC_O, 1u);
+                        }
+                        if (free_v) umma_commit_elected(leader, bar_at(sh.empty, v_slot));
+                        umma_commit_elected(leader, h == 0 ? bar_at(sh.o_half, w) : bar_at(sh.o_done, w));
+                        if (free_v) advance(v_slot, v_phase);
+                        no += h;
+                        h ^= 1;
+                        progressed = true;
+                    }
+                }
+                if (progressed) {
+                    limit = PollLimit();
+                } else if (__any_sync(FULL_MASK, *abort_flag)) {
+                    break;
+                } else if (__any_sync(FULL_MASK, limit.out())) {
+                    *abort_flag = 1;
+                    if (leader) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+                    break;
+                }
             }
-            __syncwarp();
-            ring += 2 * nt;
+            base[0] += (steps + 1) / 2;
+            base[1] += steps / 2;
         }
-        if (*abort_flag && lane == 0) {   // every MMA issued so far
-            umma_commit(smem_u32(&sh.drain));
+        if (__any_sync(FULL_MASK, *abort_flag)) {   // every MMA issued so far
+            umma_commit_elected(leader, smem_u32(&sh.drain));
             mbar_wait_bounded(smem_u32(&sh.drain), 0, DRAIN_LIMIT_NS);
         }
     } else {
@@ -298,13 +341,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int w = warp >> 2;                  // stream
         const int row = tid & (TT_M - 1);         // row of the stream's tile = tensor memory lane
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t s_col = lanes + TT_KT * w, o_col = lanes + Geo::O_COL + D * w;
+        const uint32_t o_col = lanes + Geo::O_COL + D * w;
         // a zero scale would turn the masked -inf into NaN: the smallest normal
         // numbers leave every weight of a row at 1 just as well
         const float sl2 = a.scale_log2 == 0.f ? 1e-37f : a.scale_log2;
+        const uint32_t s_col = lanes + TT_KT * w;
         uint32_t ring = 0, tiles = 0, use = 0;    // ring position and tile of the run's start; the stream's steps
         while (walk.next(a, r)) {
-            const bool two = r.rows > TT_M;
+            const bool two = r.per_tile == 2;
             const int nt = r.t1 - r.t0;
             // Q: one or two tiles of 128 rows; rows past the unit's are zero
             {
@@ -343,67 +387,60 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int pre = r.ctx - r.n;
             float m = NEG_INF, l = 0.f;
             bool ok = __all_sync(FULL_MASK, !*abort_flag);
-            const int step = two ? 1 : 2;
-            int taken = 0;                                  // tiles of the run this stream took
-            for (int j = two ? 0 : w; j < nt && ok; j += step, ++taken) {
+            int taken = 0;                                  // the stream's steps in this run
+            for (int j = two ? 0 : w; j < nt && ok; j += two ? 1 : 2, ++taken, ++use) {
                 const uint32_t mi = (tiles + j) % TT_MASKS;
                 const uint32_t vg = ring + 2 * j + 1, vslot = vg % TT_SLOTS;
                 bool ready = tt_wait(&sh.masked[mi], ((tiles + j) / TT_MASKS) & 1u, abort_flag, a.dev_err);
-                const uint4 in = *reinterpret_cast<const uint4*>(sh.mask[mi]);
+                const uint4 in4 = *reinterpret_cast<const uint4*>(sh.mask[mi]);
                 ready = ready && tt_wait(&sh.s_full[w], use & 1u, abort_flag, a.dev_err);
-                const uint32_t inw[4] = {in.x, in.y, in.z, in.w};
-                const bool all_in = (in.x & in.y & in.z & in.w) == 0xffffffffu;
+                const bool all_in = (in4.x & in4.y & in4.z & in4.w) == 0xffffffffu;
                 if (!all_in) ready = ready && tt_wait(&sh.full[vslot], (vg / TT_SLOTS) & 1u, abort_flag, a.dev_err);
                 if (!__all_sync(FULL_MASK, ready)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after_sync();
+                // value rows of tokens that take no part may hold anything, NaN too:
+                // zero them, so that 0 * V stays 0 (two row tiles share the slot:
+                // stream 0's P.V comes first, and its warps do it)
+                if (!all_in && (!two || w == 0)) {
+                    uint8_t* vs = smem + Geo::OFF_SLOTS + vslot * Geo::SLOT;
+                    for (int i = row; i < TT_KT * NH * 8; i += TT_M) {
+                        const int tok = i / (NH * 8), ch = i % (NH * 8);
+                        if (!((sh.mask[mi][tok >> 5] >> (tok & 31)) & 1u))
+                            *reinterpret_cast<uint4*>(vs + (tok / 8) * Geo::GROUP + (ch / 8) * 1024 + (tok % 8) * 128 + (ch % 8) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
                 const int p0 = (r.t0 + j) * TT_KT;
                 if (busy) {
-                    // S is read twice, 32 columns at a time and the next 32 under way:
-                    // for the maximum, then for the weights (128 cycles more of tensor
-                    // memory reads, 64 registers instead of 128)
-                    uint32_t buf[2][32];
-                    const bool every = all_in && p0 + TT_KT <= pre;   // every token seen by every row
-                    float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-                    tmem_issue32(s_col, buf[0]);
-#pragma unroll
-                    for (int c = 0; c < TT_SEQ_WORDS; ++c) {
-                        uint32_t(&x)[32] = buf[c & 1];
-                        tmem_await32(x);
-                        if (c + 1 < TT_SEQ_WORDS) tmem_issue32(s_col + 32 * (c + 1), buf[(c + 1) & 1]);
-                        if (every) {
-                            // the largest x * sl2: the largest x, or the smallest under a negative scale
-                            if (sl2 >= 0.f) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[k]));
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], -__uint_as_float(x[k]));
-                            }
-                        } else {
-                            const uint32_t seen = inw[c] & tree_bits(mrow, a.mask_words32, p0 + 32 * c - pre);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if ((seen >> k) & 1u) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[k]) * sl2);
-                        }
-                    }
-                    float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    if (every) mx *= fabsf(sl2);
-                    const bool up = mx > m + RESCALE_THRESHOLD;
-                    float alpha = 1.f;
-                    if (up) {
-                        alpha = exp2_approx(m - mx);
-                        m = mx;
-                        l *= alpha;
-                    }
-                    const float base = m == NEG_INF ? 0.f : m;
                     const float unseen = sl2 >= 0.f ? NEG_INF : INFINITY;   // times the scale: -inf
-                    // O may be rescaled only between this stream's P.V steps
-                    if (taken > 0 && __any_sync(FULL_MASK, up)) {
-                        const bool done = tt_wait(&sh.o_done[w], (use - 1) & 1u, abort_flag, a.dev_err);
-                        if (__all_sync(FULL_MASK, done)) {
+                    // One pass over S, 32 columns at a time with the next 32 under way:
+                    // the running maximum is raised (lazily, by more than
+                    // RESCALE_THRESHOLD) before a chunk's weights are taken, and then
+                    // everything before that chunk is scaled down: the sum, O, and the
+                    // step's weights already written.  That is rare after a run's
+                    // first tiles; a pass of its own for the maximum took a quarter of
+                    // the softmax's time.
+                    const bool every = all_in && p0 + TT_KT <= pre;   // every token seen by every row
+                    f32x2 sum(0.f, 0.f);
+                    auto raise = [&](float mx, int c) {   // called by the whole warp
+                        const bool up = mx > m + RESCALE_THRESHOLD;
+                        const float alpha = up ? exp2_approx(m - mx) : 1.f;
+                        if (up) m = mx;
+                        l *= alpha;
+                        sum = fma2(sum, f32x2(alpha, alpha), f32x2(0.f, 0.f));
+                        // O may be scaled only when none of this stream's P.V runs: before
+                        // this step's first half is handed over, or when that is done
+                        if (taken > 0 || c >= 2) {
+                            const bool done = c < 2 ? tt_wait(&sh.o_done[w], (use - 1) & 1u, abort_flag, a.dev_err)
+                                                    : tt_wait(&sh.o_half[w], use & 1u, abort_flag, a.dev_err);
+                            if (!__all_sync(FULL_MASK, done)) {
+                                ok = false;
+                                return;
+                            }
                             tmem_fence_after_sync();
 #pragma unroll 1
                             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -413,54 +450,85 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                                 for (int k = 0; k < 32; ++k) o[k] *= alpha;
                                 tmem_store32(o_col + c0, o);
                             }
-                        } else {
-                            ok = false;
                         }
-                    }
-                    // weights over S, 32 tokens at a time: 16 columns of hi = bf16(p),
-                    // then 16 of lo = bf16(p - hi)
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    tmem_issue32(s_col, buf[0]);
+                        tmem_await_stores();
+#pragma unroll 1
+                        for (int b = c & ~1; b < c; ++b) {   // this half's chunk before
+                            uint32_t pw[32];
+                            tmem_issue32(s_col + 32 * b, pw);
+                            tmem_await32(pw);
 #pragma unroll
-                    for (int c = 0; c < TT_SEQ_WORDS; ++c) {
-                        uint32_t(&x)[32] = buf[c & 1];
-                        tmem_await32(x);
-                        if (c + 1 < TT_SEQ_WORDS) tmem_issue32(s_col + 32 * (c + 1), buf[(c + 1) & 1]);
+                            for (int k = 0; k < 16; ++k) {
+                                const float p = (bf16_lo(pw[k]) + bf16_lo(pw[16 + k])) * alpha;
+                                const float q = (bf16_hi(pw[k]) + bf16_hi(pw[16 + k])) * alpha;
+                                pw[k] = pack_bf16(p, q);
+                                pw[16 + k] = pack_bf16(p - bf16_lo(pw[k]), q - bf16_hi(pw[k]));
+                            }
+                            tmem_store32_bits(s_col + 32 * b, pw);
+                        }
+                    };
+                    auto chunk = [&](uint32_t(&x)[32], int c) {
                         if (!every) {
-                            const uint32_t seen = inw[c] & tree_bits(mrow, a.mask_words32, p0 + 32 * c - pre);
+                            const uint32_t seen = sh.mask[mi][c] & tree_bits(mrow, a.mask_words32, p0 + 32 * c - pre);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 if (!((seen >> k) & 1u)) x[k] = __float_as_uint(unseen);
                         }
+                        // the largest x * sl2: the largest x, or the smallest under a negative scale
+                        float top[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(x[k]);
+                        if (sl2 >= 0.f) {
+#pragma unroll
+                            for (int k = 4; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[k]));
+                            top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        } else {
+#pragma unroll
+                            for (int k = 4; k < 32; ++k) top[k & 3] = fminf(top[k & 3], __uint_as_float(x[k]));
+                            top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3]));
+                        }
+                        const float mx = top[0] * sl2;
+                        if (__any_sync(FULL_MASK, mx > m + RESCALE_THRESHOLD)) raise(mx, c);
+                        // weights over S: 16 columns of hi = bf16(p), then 16 of lo = bf16(p - hi)
+                        const float base = m == NEG_INF ? 0.f : m;
+                        const f32x2 mul(sl2, sl2), sub(-base, -base), minus(-1.f, -1.f);
                         uint32_t pw[32];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const float p = exp2_approx(fmaf(__uint_as_float(x[2 * k]), sl2, -base));
-                            const float q = exp2_approx(fmaf(__uint_as_float(x[2 * k + 1]), sl2, -base));
-                            sum[k & 3] += p + q;
+                            float p, q;
+                            fma2(f32x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), mul, sub).get(p, q);
+                            p = exp2_approx(p);
+                            q = exp2_approx(q);
+                            const f32x2 pq(p, q);
+                            sum = add2(sum, pq);
                             pw[k] = pack_bf16(p, q);
-                            pw[16 + k] = pack_bf16(p - bf16_lo(pw[k]), q - bf16_hi(pw[k]));
+                            fma2(f32x2(bf16_lo(pw[k]), bf16_hi(pw[k])), minus, pq).get(p, q);
+                            pw[16 + k] = pack_bf16(p, q);
                         }
-                        tmem_store32_bits(s_col + 32 * c, pw);
+                        tmem_issue_store32(s_col + 32 * c, pw);
+                    };
+                    uint32_t x0[32], x1[32];
+                    tmem_issue32(s_col, x0);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        tmem_await32(x0);
+                        tmem_issue32(s_col + 32 * (c + 1), x1);
+                        chunk(x0, c);
+                        tmem_await32(x1);
+                        if (c == 0) tmem_issue32(s_col + TT_HT, x0);
+                        chunk(x1, c + 1);
+                        tmem_await_stores();
+                        tmem_fence_before_sync();
+                        mbar_arrive(smem_u32(&sh.p_full[w][c >> 1]));
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float s0, s1;
+                    sum.get(s0, s1);
+                    l += s0 + s1;
+                } else {
+                    tmem_fence_before_sync();
+                    mbar_arrive(smem_u32(&sh.p_full[w][0]));
+                    mbar_arrive(smem_u32(&sh.p_full[w][1]));
                 }
-                // value rows of tokens that take no part may hold anything, NaN
-                // too: zero them, so that 0 * V stays 0 (two row tiles share the
-                // slot: stream 0's P.V comes first, and its warps do it)
-                if (!all_in && (!two || w == 0)) {
-                    uint8_t* vs = smem + Geo::OFF_SLOTS + vslot * Geo::SLOT;
-                    for (int i = row; i < TT_KT * NH * 8; i += TT_M) {
-                        const int tok = i / (NH * 8), ch = i % (NH * 8);
-                        if (!((inw[tok >> 5] >> (tok & 31)) & 1u))
-                            *reinterpret_cast<uint4*>(vs + (ch / 8) * Geo::KV_HALF + tok * 128 + (ch % 8) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                }
-                tmem_fence_before_sync();
-                mbar_arrive(smem_u32(&sh.p_full[w]));
-                ++use;
             }
             // the run's last P.V of this stream
             if (ok && taken > 0) ok = tt_wait(&sh.o_done[w], (use - 1) & 1u, abort_flag, a.dev_err);
@@ -485,7 +553,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const bool go = __all_sync(FULL_MASK, ok && !*abort_flag);
             if (go && busy) {
                 const bool whole = r.t0 == 0 && r.t1 == r.nt;
-                const bool both = !two && nt > 1;
                 const int slot = 2 * blockIdx.x + (r.starts ? 0 : 1);
                 const int col0 = two ? 0 : w * (D / 2), cols = two ? D : D / 2;
                 const uint32_t first = lanes + Geo::O_COL + (two ? D * w : 0);
@@ -500,7 +567,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     tmem_load32(first + c, o);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] *= f0;
-                    if (both) {
+                    if (!two && nt > 1) {   // stream 1 took a tile
                         float o1[32];
                         tmem_load32(first + D + c, o1);
 #pragma unroll
@@ -541,8 +608,8 @@ template <int D>
 int launch(const TreeArgs& a, int ctas, cudaStream_t st) {
     static KernelSlot slot;
     CUtensorMap tk, tv;
-    if (!encode_pool_map(&tk, a.k_cache, a.num_blocks, a.num_kv_heads, a.block_size, D, a.block_size) ||
-        !encode_pool_map(&tv, a.v_cache, a.num_blocks, a.num_kv_heads, a.block_size, D, a.block_size))
+    if (!encode_block_map(&tk, a.k_cache, a.num_blocks, a.num_kv_heads, a.block_size, D) ||
+        !encode_block_map(&tv, a.v_cache, a.num_blocks, a.num_kv_heads, a.block_size, D))
         return PA_ERR_CUDA;
     const int smem = TreeGeom<D>::BYTES + 1024;
     auto kern = tree_tc_kernel<D>;

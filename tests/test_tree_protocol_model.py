@@ -28,15 +28,15 @@ class TreeSim(Sim):
         self.empty = [Barrier(f"empty[{i}]") for i in range(SLOTS)]
         self.masked = [Barrier(f"masked[{i}]") for i in range(masks)]
         self.mask = [None] * masks
-        self.s_full = [Barrier(f"s_full[{w}]") for w in range(2)]
-        self.p_full = [Barrier(f"p_full[{w}]") for w in range(2)]
-        self.o_done = [Barrier(f"o_done[{w}]") for w in range(2)]
+        one = lambda n: [Barrier(f"{n}[{w}]") for w in range(2)]  # noqa: E731
+        self.s_full, self.o_half, self.o_done = one("s_full"), one("o_half"), one("o_done")
+        self.p_full = [[Barrier(f"p_full[{w}][{h}]") for h in range(2)] for w in range(2)]
         self.reading = [0, 0]     # P.V issued and not finished, per stream
 
-    def finish_pv(self, w):
+    def finish_pv(self, w, bar):
         def done():
             self.reading[w] -= 1
-            self.o_done[w].arrive()
+            bar.arrive()
         at = max(self.mma_free_at, self.now) + 1
         self.seq += 1
         self.events.append((at, self.seq, done))
@@ -62,34 +62,39 @@ def loader(sim, runs):
 
 
 def mma(sim, runs):
-    ring, uses = 0, [0, 0]
+    ring, base = 0, [0, 0]
     for nt, two in runs:
         yield "sync"
         steps = 2 * nt if two else nt
-        ns = no = 0
+        ns = no = h = 0
         k_at = lambda i: ring + 2 * (i >> 1 if two else i)  # noqa: E731
+        use = lambda i: base[i & 1] + (i >> 1)  # noqa: E731
         landed = lambda g: sim.full[g % SLOTS].passed(g // SLOTS)  # noqa: E731
         while no < steps:
-            if ns < steps and landed(k_at(ns)) and \
-                    (ns < 2 or (no > ns - 2 and (sim.early_s or sim.o_done[ns & 1].passed(uses[ns & 1] - 1)))):
-                if sim.reading[ns & 1]:
+            w = ns & 1
+            if ns < steps and ns < no + 2 + sim.early_s and landed(k_at(ns)) and \
+                    (ns < 2 or sim.early_s or sim.o_done[w].passed(use(ns) - 1)):
+                if sim.reading[w]:
                     raise AssertionError("S issued over weights that a P.V still reads")
                 sim.mma(5)
-                sim.commit(sim.s_full[ns & 1])
-                if not two or ns & 1:
+                sim.commit(sim.s_full[w])
+                if not two or w:
                     sim.commit(sim.empty[k_at(ns) % SLOTS])
                 ns += 1
-            if no < ns and sim.p_full[no & 1].passed(uses[no & 1]) and landed(k_at(no) + 1):
-                sim.mma(10)
-                sim.reading[no & 1] += 1
-                if not two or no & 1:
+            w = no & 1
+            if no < ns and sim.p_full[w][h].passed(use(no)) and (h or landed(k_at(no) + 1)):
+                sim.mma(5)
+                sim.reading[w] += 1
+                if h and (not two or w):
                     sim.commit(sim.empty[(k_at(no) + 1) % SLOTS])
-                sim.finish_pv(no & 1)
-                uses[no & 1] += 1
-                no += 1
+                sim.finish_pv(w, sim.o_done[w] if h else sim.o_half[w])
+                no += h
+                h ^= 1
             yield
             yield from sim.pause(2)
         ring += 2 * nt
+        base[0] += (steps + 1) // 2
+        base[1] += steps // 2
 
 
 def softmax(sim, runs, w):
@@ -109,11 +114,17 @@ def softmax(sim, runs, w):
                 g = ring + 2 * j + 1
                 while not sim.full[g % SLOTS].passed(g // SLOTS):
                     yield
-            if taken and sim.rng.random() < 0.3:   # rescale
-                while not sim.o_done[w].passed(use - 1):
-                    yield
-            yield from sim.pause(8)
-            sim.p_full[w].arrive()
+            for h in range(2):
+                if (h or taken) and sim.rng.random() < 0.3:   # O scaled: none of its P.V may run
+                    bar, phase = (sim.o_half[w], use) if h else (sim.o_done[w], use - 1)
+                    while not bar.passed(phase):
+                        yield
+                    if sim.reading[w]:
+                        raise AssertionError("O scaled while a P.V adds to it")
+                yield from sim.pause(5)
+                if sim.mask[t % sim.masks] != t:
+                    raise AssertionError("a token mask was overwritten before it was read")
+                sim.p_full[w][h].arrive()
             use += 1
             taken += 1
         if taken:
