@@ -10,16 +10,17 @@
 // query rows (row r = node r / g, head r % g of the group), all of which read
 // the same K/V.  It takes ceil(context / KT) K/V tiles, at least one, and a tile
 // costs one step per HALF rows (a kernel that works through ROWS = 2 HALF rows
-// needs twice the time for more than HALF of them).  The units' steps in a row
+// needs twice the time for more than HALF of them); starting and finishing a unit
+// costs another TREE_UNIT_STEPS, behind its tiles.  The units' steps in a row
 // (sequence, kv head, row block) form a line of W steps that the CTAs cut into
 // equal shares: CTA c of G takes the tiles whose first step lies in [c W / G,
 // (c + 1) W / G).  Ragged contexts and drafts need no other balancing, few rows
 // over a long context are split as finely as there are SMs, and a CTA leaves at
 // most two units unfinished: a partial (max, sum, unnormalised output) for its
 // first run and one for its last, whatever the batch.  A second kernel joins
-// each cut unit's partials in CTA order.  Shares have at least two steps, so that
-// each holds the start of a tile.  The cuts depend on the whole batch, so a row's
-// rounding may differ in another batch; a batch gives the same bits every time.
+// each cut unit's partials in CTA order.  The cuts depend on the whole batch, so a
+// row's rounding may differ in another batch; a batch gives the same bits every
+// time.
 #pragma once
 
 #include "pa_device.cuh"
@@ -27,12 +28,11 @@
 
 namespace pa {
 
-// The run a CTA's share starts with, for the join.
+// The run a CTA's share starts with, for the join (none: t0 = 0, begin = -1).
 struct TreeRecord {
-    long long begin;             // the unit's first step on the line
+    int begin;                   // the unit's first step on the line
     int first, kvh, row0, rows;  // its rows (see TreeRun)
     int t0, nt, per_tile;        // the run's first tile, the unit's tiles, steps per tile
-    int pad;
 };
 
 struct TreeArgs {
@@ -46,7 +46,7 @@ struct TreeArgs {
     const uint32_t* tree_mask;   // [num_tokens][mask_words32]
     int32_t* dev_err;
     TreeRecord* recs;            // [CTA]: the unit each CTA's share starts in
-    long long* line;             // W
+    int* line;                   // W
     float* part_acc;             // [2 * CTA][head_dim / 4][part_rows][4]
     float2* part_ml;             // [2 * CTA][part_rows]
     int part_rows;               // rows a partial has room for
@@ -61,6 +61,8 @@ struct TreeArgs {
 constexpr int TREE_CTAS_MAX = 160;
 // Sequences are found in windows of 32; the windows' sums sit in shared memory.
 constexpr int TREE_WINDOWS_MAX = 4096;
+// What a unit costs besides its tiles (the host bounds W by INT_MAX).
+constexpr int TREE_UNIT_STEPS = 2;
 
 // One sequence as the work line sees it; a malformed one (rows outside q) has none.
 struct TreeSeq {
@@ -87,15 +89,17 @@ __device__ __forceinline__ int tree_tiles(int ctx) {
     return ctx > 0 ? (ctx - 1) / KT + 1 : 1;   // an empty context still writes its zero rows
 }
 
-// Steps of a sequence's units, and of one kv head's: row blocks of two halves,
-// the last one of one half when that holds its rows.
+// Row blocks of a sequence and kv head, in halves of HALF rows; all blocks but the
+// last have HALVES of them.
 template <int HALF>
 __device__ __forceinline__ int tree_halves(const TreeArgs& a, int n) {
     return (n * a.group + HALF - 1) / HALF;
 }
-template <int HALF, int KT>
-__device__ __forceinline__ long long tree_cost(const TreeArgs& a, const TreeSeq& t) {
-    return static_cast<long long>(tree_halves<HALF>(a, t.n)) * a.num_kv_heads * tree_tiles<KT>(t.ctx);
+// Steps of one kv head's units.
+template <int HALF, int HALVES, int KT>
+__device__ __forceinline__ int tree_head_steps(const TreeArgs& a, const TreeSeq& t) {
+    const int halves = tree_halves<HALF>(a, t.n);
+    return halves * tree_tiles<KT>(t.ctx) + (halves + HALVES - 1) / HALVES * TREE_UNIT_STEPS;
 }
 
 // A run of one unit's tiles.
@@ -104,7 +108,7 @@ struct TreeRun {
     int kvh, row0, rows;    // kv head; the unit's first row and rows within (node, head) rows
     int t0, t1, nt;         // tiles [t0, t1) of the unit's nt
     int per_tile;           // steps per tile (1 or 2)
-    long long begin;        // the unit's first step on the line
+    int begin;              // the unit's first step on the line
     bool starts;            // the CTA's first run
 };
 
@@ -113,24 +117,18 @@ struct TreeRun {
 template <int HALF, int HALVES, int KT>
 struct TreeWalker {
     static_assert(HALVES == 1 || HALVES == 2, "steps per tile");
-    long long w, w_end;     // position on the line, the end of the CTA's share
+    int w, w_end;           // position on the line, the end of the CTA's share
     int seq0;               // the window's first sequence
     bool started;           // a run was given out
     TreeSeq mine;
-    long long start, cost;  // the lane's sequence on the line
+    int start, cost;        // the lane's sequence on the line
 
-    __device__ __forceinline__ void load(const TreeArgs& a, int first_seq, long long at) {
+    __device__ __forceinline__ void load(const TreeArgs& a, int first_seq, int at) {
         const int lane = threadIdx.x & 31;
         seq0 = first_seq;
         mine = tree_seq(a, seq0 + lane, false);
-        cost = tree_cost<HALF, KT>(a, mine);
-        long long inc = cost;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(FULL_MASK, inc, o);
-            if (lane >= o) inc += v;
-        }
-        start = at + inc - cost;
+        cost = tree_head_steps<HALF, HALVES, KT>(a, mine) * a.num_kv_heads;
+        start = at + warp_inclusive_scan(cost) - cost;
     }
 
     // The next run, or false at the end of the CTA's share.  Called by all lanes.
@@ -146,28 +144,30 @@ struct TreeWalker {
             r.first = __shfl_sync(FULL_MASK, mine.first, l);
             r.n = __shfl_sync(FULL_MASK, mine.n, l);
             r.ctx = __shfl_sync(FULL_MASK, mine.ctx, l);
-            const long long seq_start = __shfl_sync(FULL_MASK, start, l);
             r.nt = tree_tiles<KT>(r.ctx);
-            // kv head, then row block: all of HALVES steps per tile but the last
-            const int halves = tree_halves<HALF>(a, r.n);
-            const long long head_steps = static_cast<long long>(halves) * r.nt;
-            long long off = w - seq_start;
-            r.kvh = static_cast<int>(off / head_steps);
+            unsigned off = w - __shfl_sync(FULL_MASK, start, l);
+            const unsigned seq_steps = __shfl_sync(FULL_MASK, cost, l);
+            // overlapping ranges of a malformed query_start can overflow the line:
+            // nothing outside a sequence's own steps is ever a run
+            if (off >= seq_steps) return false;
+            const unsigned head_steps = seq_steps / a.num_kv_heads;
+            r.kvh = off / head_steps;
             off -= r.kvh * head_steps;
-            const long long block_steps = static_cast<long long>(HALVES) * r.nt;
-            const int block = static_cast<int>(off / block_steps);
+            const unsigned block_steps = HALVES * r.nt + TREE_UNIT_STEPS;
+            const int block = off / block_steps;
             off -= block * block_steps;
-            r.per_tile = min(HALVES, halves - HALVES * block);
+            r.per_tile = min(HALVES, tree_halves<HALF>(a, r.n) - HALVES * block);
             r.row0 = block * HALF * HALVES;
             r.rows = min(HALF * HALVES, r.n * a.group - r.row0);
             r.begin = w - off;
             // tiles whose first step is in the share
-            const long long unit_steps = static_cast<long long>(r.per_tile) * r.nt;
-            const long long end = r.begin + unit_steps < w_end ? unit_steps : w_end - r.begin;
-            r.t0 = static_cast<int>((off + r.per_tile - 1) / r.per_tile);
-            r.t1 = static_cast<int>((end + r.per_tile - 1) / r.per_tile);
+            const int unit_steps = r.per_tile * r.nt + TREE_UNIT_STEPS;
+            const int end = min(unit_steps, w_end - r.begin);
+            r.t0 = min(r.nt, (static_cast<int>(off) + r.per_tile - 1) / r.per_tile);
+            r.t1 = min(r.nt, (end + r.per_tile - 1) / r.per_tile);
+            if (r.begin + end <= w) return false;
             w = r.begin + end;
-            if (r.t0 >= r.t1) continue;   // only the second step of a tile whose first is another CTA's
+            if (r.t0 >= r.t1) continue;   // the share holds no tile's first step of this unit
             r.starts = !started;
             started = true;
             return true;
@@ -177,11 +177,9 @@ struct TreeWalker {
 };
 
 // CTAs that share a line of W steps, and the first step of CTA c's share.
-__device__ __forceinline__ int tree_sharers(long long W, int ctas) {
-    return W / 2 < ctas ? (W > 1 ? static_cast<int>(W / 2) : 1) : ctas;
-}
-__device__ __forceinline__ long long tree_share(long long W, int sharers, int c) {
-    return c >= sharers ? W : W / sharers * c + (W % sharers) * c / sharers;
+__device__ __forceinline__ int tree_sharers(int W, int ctas) { return W / 2 < ctas ? (W > 1 ? W / 2 : 1) : ctas; }
+__device__ __forceinline__ int tree_share(int W, int sharers, int c) {
+    return c >= sharers ? W : W / sharers * c + W % sharers * c / sharers;
 }
 
 // Line length and the CTA's walker.  Called by the whole CTA; `sums` (shared
@@ -189,17 +187,17 @@ __device__ __forceinline__ long long tree_share(long long W, int sharers, int c)
 // next barrier.  CTA 0 reports malformed sequences and keeps the length for the
 // join.
 template <int HALF, int HALVES, int KT>
-__device__ __forceinline__ void tree_begin(const TreeArgs& a, long long* sums, TreeWalker<HALF, HALVES, KT>& walk) {
+__device__ __forceinline__ void tree_begin(const TreeArgs& a, int* sums, TreeWalker<HALF, HALVES, KT>& walk) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
     const int windows = (a.num_seqs + 31) / 32;
     for (int v = warp; v < windows; v += nwarps) {
-        long long c = tree_cost<HALF, KT>(a, tree_seq(a, 32 * v + lane, blockIdx.x == 0));
+        int c = tree_head_steps<HALF, HALVES, KT>(a, tree_seq(a, 32 * v + lane, blockIdx.x == 0)) * a.num_kv_heads;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(FULL_MASK, c, o);
         if (lane == 0) sums[v] = c;
     }
     __syncthreads();
-    long long total = 0;
+    int total = 0;
     for (int v = lane; v < windows; v += 32) total += sums[v];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(FULL_MASK, total, o);
@@ -208,15 +206,18 @@ __device__ __forceinline__ void tree_begin(const TreeArgs& a, long long* sums, T
     walk.w_end = tree_share(total, sharers, blockIdx.x + 1);
     walk.started = false;
     // the window that holds the first step of the share
-    long long at = 0;
-    int v = 0;
+    int at = 0, v = 0;
     while (v + 1 < windows && at + sums[v] <= walk.w) at += sums[v++];
     walk.load(a, 32 * v, at);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.line = total;
+    if (threadIdx.x == 0) {
+        if (blockIdx.x == 0) *a.line = total;
+        a.recs[blockIdx.x] = TreeRecord{-1, 0, 0, 0, 0, 0, 0, 1};
+    }
 }
 
+// Called after the barrier that follows tree_begin, by one thread.
 __device__ __forceinline__ void tree_record(const TreeArgs& a, const TreeRun& r) {
-    a.recs[blockIdx.x] = TreeRecord{r.begin, r.first, r.kvh, r.row0, r.rows, r.t0, r.nt, r.per_tile, 0};
+    a.recs[blockIdx.x] = TreeRecord{r.begin, r.first, r.kvh, r.row0, r.rows, r.t0, r.nt, r.per_tile};
 }
 
 __device__ __forceinline__ float* tree_part(const TreeArgs& a, int slot, int D) {

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(TS_THREADS) tree_simt_kernel(const TreeArgs a)
     pdl_wait();
     pdl_launch_dependents();
     TreeWalker<TS_ROWS, 1, TS_KT> walk;
-    tree_begin(a, reinterpret_cast<long long*>(smem_dyn), walk);
+    tree_begin(a, reinterpret_cast<int*>(smem_dyn), walk);
     __syncthreads();
 
     TreeRun r;
@@ -256,33 +256,50 @@ constexpr int TJ_ROWS = 32;   // rows per CTA
 
 template <int D>
 __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const TreeArgs a, int ctas) {
-    __shared__ float s_coef[TJ_ROWS][TREE_CTAS_MAX + 1];   // weight of each partial, then 1 / sum
+    __shared__ float s_coef[TJ_ROWS][TREE_CTAS_MAX + 1];   // weight of each partial
+    __shared__ int s_slot[TREE_CTAS_MAX];
+    __shared__ int s_parts;
     pdl_wait();
     pdl_launch_dependents();
     const int c = blockIdx.x + 1;   // share 0 starts no cut
-    const long long W = *a.line;
-    const int g = tree_sharers(W, ctas);
-    if (c >= g) return;
+    const int W = *a.line;
     const TreeRecord r = a.recs[c];
-    if (r.t0 == 0) return;                               // the share starts with a unit
-    if (tree_share(W, g, c - 1) > r.begin) return;       // not the unit's first cut
+    const int g = tree_sharers(W, ctas);
+    if (c >= g || r.t0 == 0) return;                     // no share, or it starts with a unit
     const int row0 = blockIdx.y * TJ_ROWS, here = min(TJ_ROWS, r.rows - row0);
     if (here <= 0) return;
-    // partials: CTA c - 1's (its first run if its share starts with the unit), then
-    // those of c .. last, which start inside it
-    int last = c;
-    const long long last_tile = r.begin + static_cast<long long>(r.nt - 1) * r.per_tile;
-    while (last + 1 < g && tree_share(W, g, last + 1) <= last_tile) ++last;
-    const int head = 2 * (c - 1) + (a.recs[c - 1].begin == r.begin ? 0 : 1);
-    const int parts = last - c + 2;
-    auto slot_of = [&](int p) { return p == 0 ? head : 2 * (c - 1 + p); };
+    // the tiles [t0, t1) that share x holds of this unit
+    auto first_tile = [&](int x) {
+        const int off = tree_share(W, g, x) - r.begin;
+        return off <= 0 ? 0 : min(r.nt, (off + r.per_tile - 1) / r.per_tile);
+    };
+    // the unit's tile 0 lies in the nearest share before c that holds a tile of it;
+    // c joins the unit if that one is it, i.e. starts with or before the unit
+    int head = c - 1;
+    while (first_tile(head) == r.t0) --head;             // no tile of its own
+    if (first_tile(head) > 0) return;                    // not the unit's first cut
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int head_slot = 2 * head + (a.recs[head].begin == r.begin ? 0 : 1);
+        int n = 1;
+        if (lane == 0) s_slot[0] = head_slot;
+        for (int x0 = c; x0 < g && first_tile(x0) < r.nt; x0 += 32) {
+            const int x = x0 + lane;
+            const bool has = x < g && first_tile(x) < first_tile(x + 1);
+            const unsigned all = __ballot_sync(FULL_MASK, has);
+            if (has) s_slot[n + __popc(all & ((1u << lane) - 1u))] = 2 * x;
+            n += __popc(all);
+        }
+        if (lane == 0) s_parts = n;
+    }
+    __syncthreads();
+    const int parts = s_parts;
     if (threadIdx.x < here) {
         const int row = row0 + threadIdx.x;
         float M = NEG_INF, L = 0.f;
-        for (int p = 0; p < parts; ++p)
-            M = fmaxf(M, a.part_ml[static_cast<size_t>(slot_of(p)) * a.part_rows + row].x);
+        for (int p = 0; p < parts; ++p) M = fmaxf(M, a.part_ml[static_cast<size_t>(s_slot[p]) * a.part_rows + row].x);
         for (int p = 0; p < parts; ++p) {
-            const float2 ml = a.part_ml[static_cast<size_t>(slot_of(p)) * a.part_rows + row];
+            const float2 ml = a.part_ml[static_cast<size_t>(s_slot[p]) * a.part_rows + row];
             const float e = M == NEG_INF ? 0.f : exp2_approx(ml.x - M);
             s_coef[threadIdx.x][p] = e;
             L = fmaf(e, ml.y, L);
@@ -297,7 +314,7 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const TreeArgs a,
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int p = 0; p < parts; ++p) {
             const float e = s_coef[rr][p];
-            const float4 v = reinterpret_cast<const float4*>(tree_part(a, slot_of(p), D))[c4 * a.part_rows + row0 + rr];
+            const float4 v = reinterpret_cast<const float4*>(tree_part(a, s_slot[p], D))[c4 * a.part_rows + row0 + rr];
             o.x = fmaf(e, v.x, o.x);
             o.y = fmaf(e, v.y, o.y);
             o.z = fmaf(e, v.z, o.z);
@@ -367,6 +384,13 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
         static_cast<long long>(num_tokens) * num_heads > INT_MAX || num_seqs > 32 * TREE_WINDOWS_MAX)
         return PA_ERR_UNSUPPORTED;
     if (static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX) return PA_ERR_INVALID_ARG;
+    long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
+    if (max_context_len > 0 && max_context_len < cap) cap = max_context_len;
+    // the work line is counted in 32 bits: at most this many half row blocks, each
+    // with a step per 64-token tile
+    const long long halves = static_cast<long long>(num_tokens) * num_heads / TS_ROWS +
+                             static_cast<long long>(num_seqs) * num_kv_heads;
+    if (halves > INT_MAX / (cap / TS_KT + 1 + TREE_UNIT_STEPS)) return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PA_OK;
     if (num_seqs == 0) return PA_ERR_INVALID_ARG;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !tree_mask || !workspace)
@@ -378,8 +402,6 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
     const TreeWs L = tree_ws(num_tokens, num_heads, head_dim);
     if (workspace_bytes < L.total) return PA_ERR_WORKSPACE;
 
-    long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
-    if (max_context_len > 0 && max_context_len < cap) cap = max_context_len;
     TreeArgs a;
     a.out = out;
     a.q = q;
@@ -391,7 +413,7 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
     a.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
     a.dev_err = dev_err;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.line = reinterpret_cast<long long*>(ws + L.line);
+    a.line = reinterpret_cast<int*>(ws + L.line);
     a.recs = reinterpret_cast<TreeRecord*>(ws + L.recs);
     a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
     a.part_acc = reinterpret_cast<float*>(ws + L.acc);

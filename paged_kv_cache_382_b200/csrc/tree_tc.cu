@@ -80,7 +80,7 @@ struct TreeGeom {
     // tensor memory columns: S / P of stream w at 128 w, O of stream w behind both
     static constexpr int O_COL = 2 * TT_KT;
     static_assert(O_COL + 2 * D <= TT_TMEM_COLS, "tensor memory");
-    static_assert(TREE_WINDOWS_MAX * 8 <= TT_SLOTS * SLOT, "window sums fit the ring");
+    static_assert(TREE_WINDOWS_MAX * 4 <= TT_SLOTS * SLOT, "window sums fit the ring");
 };
 
 constexpr uint32_t TT_IDESC_S = umma_idesc_bf16(TT_M, TT_KT, 0, 0);
@@ -124,6 +124,45 @@ __device__ __forceinline__ bool tt_wait(uint64_t* bar, uint32_t parity, volatile
     return true;
 }
 
+// A row's maximum was raised before chunk c of a step: scales what was summed with
+// the old one, O (when scale_o, once `bar` says that none of the stream's P.V runs)
+// and the weights of the chunk before c that were not handed over yet.  Out of
+// line: it is rare, and the loop that calls it has to stay small for the
+// instruction caches (inlined, the softmax took 1.3 times as long).
+template <int D>
+__device__ __noinline__ bool tt_rescale(uint32_t o_col, uint32_t s_col, float alpha, int c, bool scale_o, uint64_t* bar,
+                                        uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
+    if (scale_o) {
+        const bool done = tt_wait(bar, parity, abort_flag, dev_err);
+        if (!__all_sync(FULL_MASK, done)) return false;
+        tmem_fence_after_sync();
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_load32(o_col + c0, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= alpha;
+            tmem_store32(o_col + c0, o);
+        }
+    }
+    if (c & 1) {
+        tmem_await_stores();
+        const uint32_t col = s_col + 32 * (c - 1);
+        uint32_t pw[32];
+        tmem_issue32(col, pw);
+        tmem_await32(pw);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float p = (bf16_lo(pw[k]) + bf16_lo(pw[16 + k])) * alpha;
+            const float q = (bf16_hi(pw[k]) + bf16_hi(pw[16 + k])) * alpha;
+            pw[k] = pack_bf16(p, q);
+            pw[16 + k] = pack_bf16(p - bf16_lo(pw[k]), q - bf16_hi(pw[k]));
+        }
+        tmem_store32_bits(col, pw);
+    }
+    return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(TT_THREADS, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
@@ -160,7 +199,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     pdl_wait();
     pdl_launch_dependents();
     TreeWalker<TT_M, 2, TT_KT> walk;
-    tree_begin(a, reinterpret_cast<long long*>(smem + Geo::OFF_SLOTS), walk);
+    tree_begin(a, reinterpret_cast<int*>(smem + Geo::OFF_SLOTS), walk);
     fence_proxy_async_smem();   // the window sums lie where copies land next
     tmem_fence_before_sync();
     __syncthreads();
@@ -350,29 +389,38 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         while (walk.next(a, r)) {
             const bool two = r.per_tile == 2;
             const int nt = r.t1 - r.t0;
-            // Q: one or two tiles of 128 rows; rows past the unit's are zero
+            // Q: one or two tiles of 128 rows; rows past the unit's are zero.  A thread
+            // loads chunk ch of every STRIDE-th row; (node, head) step along.
             {
-                constexpr int CH = D / 8;         // 16-byte chunks of a row
-                const int chunks = (two ? 2 : 1) * TT_M * CH;
-                constexpr int BATCH = 8;
-                for (int i0 = tid; i0 < chunks; i0 += BATCH * TT_SOFTMAX) {
+                constexpr int CH = D / 8, STRIDE = TT_SOFTMAX / CH, BATCH = 8;
+                const int ch = tid % CH, G = a.group;
+                const int by_node = STRIDE / G, by_head = STRIDE - by_node * G;
+                int rr = tid / CH;
+                int node = (r.row0 + rr) / G, head = r.row0 + rr - node * G;
+                const uint4* q = reinterpret_cast<const uint4*>(a.q) + ch;
+                const int rows = two ? 2 * TT_M : TT_M;
+                while (rr < rows) {
                     uint4 v[BATCH];
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k) {
-                        const int i = i0 + k * TT_SOFTMAX, rr = i / CH;
                         v[k] = make_uint4(0u, 0u, 0u, 0u);
-                        if (i < chunks && rr < r.rows)
-                            v[k] = __ldg(reinterpret_cast<const uint4*>(
-                                       static_cast<const __nv_bfloat16*>(a.q) +
-                                       tree_out_row(a, r.first, r.kvh, r.row0 + rr) * D) + i % CH);
+                        if (rr + k * STRIDE < r.rows)
+                            v[k] = __ldg(q + (static_cast<size_t>(r.first + node) * a.num_heads + r.kvh * G + head) * CH);
+                        node += by_node;
+                        head += by_head;
+                        if (head >= G) {
+                            head -= G;
+                            ++node;
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < BATCH; ++k) {
-                        const int i = i0 + k * TT_SOFTMAX, rr = i / CH, ch = i % CH;
-                        if (i < chunks)
-                            *reinterpret_cast<uint4*>(smem + (rr / TT_M) * Geo::Q_TILE + (ch / 8) * Geo::Q_HALF +
-                                                      (rr % TT_M) * 128 + (((ch % 8) ^ (rr & 7)) << 4)) = v[k];
+                        const int i = rr + k * STRIDE;
+                        if (i < rows)
+                            *reinterpret_cast<uint4*>(smem + (i / TT_M) * Geo::Q_TILE + (ch / 8) * Geo::Q_HALF +
+                                                      (i % TT_M) * 128 + (((ch % 8) ^ (i & 7)) << 4)) = v[k];
                     }
+                    rr += BATCH * STRIDE;
                 }
             }
             fence_proxy_async_smem();
@@ -418,56 +466,18 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 if (busy) {
                     const float unseen = sl2 >= 0.f ? NEG_INF : INFINITY;   // times the scale: -inf
                     // One pass over S, 32 columns at a time with the next 32 under way:
-                    // the running maximum is raised (lazily, by more than
-                    // RESCALE_THRESHOLD) before a chunk's weights are taken, and then
-                    // everything before that chunk is scaled down: the sum, O, and the
-                    // step's weights already written.  That is rare after a run's
-                    // first tiles; a pass of its own for the maximum took a quarter of
-                    // the softmax's time.
+                    // the running maximum is raised lazily (by more than
+                    // RESCALE_THRESHOLD), and then everything before the chunk is scaled
+                    // down: the sum, O, and the weights of the step not handed over yet.
+                    // That is rare after a run's first tiles; a pass of its own for the
+                    // maximum took a quarter of the softmax's time.
                     const bool every = all_in && p0 + TT_KT <= pre;   // every token seen by every row
                     f32x2 sum(0.f, 0.f);
-                    auto raise = [&](float mx, int c) {   // called by the whole warp
-                        const bool up = mx > m + RESCALE_THRESHOLD;
-                        const float alpha = up ? exp2_approx(m - mx) : 1.f;
-                        if (up) m = mx;
-                        l *= alpha;
-                        sum = fma2(sum, f32x2(alpha, alpha), f32x2(0.f, 0.f));
-                        // O may be scaled only when none of this stream's P.V runs: before
-                        // this step's first half is handed over, or when that is done
-                        if (taken > 0 || c >= 2) {
-                            const bool done = c < 2 ? tt_wait(&sh.o_done[w], (use - 1) & 1u, abort_flag, a.dev_err)
-                                                    : tt_wait(&sh.o_half[w], use & 1u, abort_flag, a.dev_err);
-                            if (!__all_sync(FULL_MASK, done)) {
-                                ok = false;
-                                return;
-                            }
-                            tmem_fence_after_sync();
+                    uint32_t x[32];
+                    tmem_issue32(s_col, x);
 #pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
-                                float o[32];
-                                tmem_load32(o_col + c0, o);
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                                tmem_store32(o_col + c0, o);
-                            }
-                        }
-                        tmem_await_stores();
-#pragma unroll 1
-                        for (int b = c & ~1; b < c; ++b) {   // this half's chunk before
-                            uint32_t pw[32];
-                            tmem_issue32(s_col + 32 * b, pw);
-                            tmem_await32(pw);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float p = (bf16_lo(pw[k]) + bf16_lo(pw[16 + k])) * alpha;
-                                const float q = (bf16_hi(pw[k]) + bf16_hi(pw[16 + k])) * alpha;
-                                pw[k] = pack_bf16(p, q);
-                                pw[16 + k] = pack_bf16(p - bf16_lo(pw[k]), q - bf16_hi(pw[k]));
-                            }
-                            tmem_store32_bits(s_col + 32 * b, pw);
-                        }
-                    };
-                    auto chunk = [&](uint32_t(&x)[32], int c) {
+                    for (int c = 0; c < TT_MASK_WORDS; ++c) {
+                        tmem_await32(x);
                         if (!every) {
                             const uint32_t seen = sh.mask[mi][c] & tree_bits(mrow, a.mask_words32, p0 + 32 * c - pre);
 #pragma unroll
@@ -480,19 +490,37 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(x[k]);
                         if (sl2 >= 0.f) {
 #pragma unroll
-                            for (int k = 4; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(x[k]));
-                            top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                            for (int k = 4; k < 28; k += 8)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    top[i] = max3(top[i], __uint_as_float(x[k + i]), __uint_as_float(x[k + 4 + i]));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __uint_as_float(x[28 + i]));
+                            top[0] = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                         } else {
 #pragma unroll
                             for (int k = 4; k < 32; ++k) top[k & 3] = fminf(top[k & 3], __uint_as_float(x[k]));
                             top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3]));
                         }
                         const float mx = top[0] * sl2;
-                        if (__any_sync(FULL_MASK, mx > m + RESCALE_THRESHOLD)) raise(mx, c);
+                        const bool up = mx > m + RESCALE_THRESHOLD;
+                        if (__any_sync(FULL_MASK, up)) {
+                            const float alpha = up ? exp2_approx(m - mx) : 1.f;
+                            if (up) m = mx;
+                            l *= alpha;
+                            sum = fma2(sum, f32x2(alpha, alpha), f32x2(0.f, 0.f));
+                            // O may be scaled only when none of this stream's P.V runs: before
+                            // this step's first half is handed over, or when that is done
+                            const bool late = c >= 2;
+                            ok &= tt_rescale<D>(o_col, s_col, alpha, c, taken > 0 || late,
+                                                late ? &sh.o_half[w] : &sh.o_done[w], late ? use & 1u : (use - 1) & 1u,
+                                                abort_flag, a.dev_err);
+                        }
                         // weights over S: 16 columns of hi = bf16(p), then 16 of lo = bf16(p - hi)
                         const float base = m == NEG_INF ? 0.f : m;
                         const f32x2 mul(sl2, sl2), sub(-base, -base), minus(-1.f, -1.f);
                         uint32_t pw[32];
+                        f32x2 part[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             float p, q;
@@ -500,26 +528,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                             p = exp2_approx(p);
                             q = exp2_approx(q);
                             const f32x2 pq(p, q);
-                            sum = add2(sum, pq);
+                            part[k & 1] = add2(part[k & 1], pq);
                             pw[k] = pack_bf16(p, q);
                             fma2(f32x2(bf16_lo(pw[k]), bf16_hi(pw[k])), minus, pq).get(p, q);
                             pw[16 + k] = pack_bf16(p, q);
                         }
+                        sum = add2(sum, add2(part[0], part[1]));
+                        if (c + 1 < TT_MASK_WORDS) tmem_issue32(s_col + 32 * (c + 1), x);
                         tmem_issue_store32(s_col + 32 * c, pw);
-                    };
-                    uint32_t x0[32], x1[32];
-                    tmem_issue32(s_col, x0);
-#pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        tmem_await32(x0);
-                        tmem_issue32(s_col + 32 * (c + 1), x1);
-                        chunk(x0, c);
-                        tmem_await32(x1);
-                        if (c == 0) tmem_issue32(s_col + TT_HT, x0);
-                        chunk(x1, c + 1);
-                        tmem_await_stores();
-                        tmem_fence_before_sync();
-                        mbar_arrive(smem_u32(&sh.p_full[w][c >> 1]));
+                        if (c & 1) {
+                            tmem_await_stores();
+                            tmem_fence_before_sync();
+                            mbar_arrive(smem_u32(&sh.p_full[w][c >> 1]));
+                        }
                     }
                     float s0, s1;
                     sum.get(s0, s1);

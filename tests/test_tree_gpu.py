@@ -345,3 +345,16 @@ def test_verify_and_commit_a_draft(pa):
             ref = oracle.decode_attention_one(f64(qd[s, h]), k[:, h // 4], v[:, h // 4], scale)
             assert np.abs(f64(dout[s, h]) - ref).max() <= 2e-3
     assert torch.equal(kc[shared].view(torch.int16), before.view(torch.int16))
+
+
+def test_tree_overlapping_ranges_stay_in_bounds(pa):
+    """A query_start that runs back and forth names rows several times: flagged, no row of another
+    sequence's range is touched, nothing faults."""
+    ctx, nodes = [40] * 6, [10, 0, 0, 0, 0, 0]
+    for dtype in (torch.bfloat16, torch.float32):
+        step, q, mask, _ = inputs(ctx, nodes, 4, 2, 64, 16, dtype, poison=False)
+        q = torch.cat([q, q])
+        mask = np.concatenate([mask, mask])
+        out, err = run(pa, step, q, mask, np.array([0, 10, 0, 10, 0, 10, 10], dtype=np.int32))
+        assert err == pa.DEVERR_CONTEXT
+        assert torch.isfinite(out[:10]).all() and torch.all(out[10:] == -77.0)
