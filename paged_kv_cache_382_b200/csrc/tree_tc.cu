@@ -3,23 +3,24 @@
 // how the work is cut into shares).
 //
 // One CTA per SM takes a share of the work line.  A unit's rows are one or two
-// MMA tiles of 128 rows; K and V come in tiles of 128 tokens.  Two streams, each
-// with its own four softmax warps, S / P buffer and O accumulator in tensor
-// memory, keep the tensor cores and the exponentials busy at once:
-//   more than 128 rows: stream w owns row tile w and takes every K/V tile, so
-//                       K and V are read once for up to 256 rows;
-//   up to 128 rows:     both streams hold the same rows, stream w takes the run's
-//                       tiles w, w + 2, ...; the epilogue joins the two.
-// Step i of a run (stream i % 2) is
-//   S = Q . K^T   (M = 128 rows, N = 128 tokens, K = d)
+// MMA tiles of 128 rows; K and V come in tiles of 128 tokens, worked through in
+// halves of 64.  Two streams, each with its own four softmax warps, two S / P
+// buffers and an O accumulator in tensor memory, keep the tensor cores and the
+// exponentials busy at once:
+//   more than 128 rows: stream w owns row tile w and takes every half, so K and V
+//                       are read once for up to 256 rows;
+//   up to 128 rows:     both streams hold the same rows, stream w takes half w of
+//                       every tile; the epilogue joins the two.
+// Step k of a stream (buffer k % 2) is
+//   S = Q . K^T   (M = 128 rows, N = 64 tokens, K = d)
 //   softmax       (online, base 2, lazy rescale of O in tensor memory)
-//   O += P . V    (M = 128, N = d, K = 128 tokens; P as a bf16 pair hi + lo,
+//   O += P . V    (M = 128, N = d, K = 64 tokens; P as a bf16 pair hi + lo,
 //                  written over S: about 16 significant bits, so that the
 //                  weights' rounding stays below the output's)
-// P is handed over in two halves of 64 tokens, so that P.V of the first runs
-// while the second is computed.  Steps of 64 tokens with two buffers per stream
-// were slower: the tensor cores lose 120 cycles at every change between the two
-// products (1440 cycles a step measured for 900 of MMAs).
+// While a stream's warps work on step k, the tensor cores do PV(k - 1) and S(k + 1)
+// in the other buffer.  One buffer of 128 tokens per stream (tensor memory holds no
+// more next to two O of d = 128) left the warps waiting for both products, a third
+// of the time.
 //
 // K and V tiles go through one ring of five 32 KB slots in the order K0 V0 K1
 // V1 ...; a K slot is free again once its S are done, so up to 160 KB are in
@@ -29,9 +30,9 @@
 // warp for both pools held an SM at 22 GB/s.
 //
 // Per 128-token tile: 64 KB of K and V, 1.5 us at an SM's share of the measured
-// copy bandwidth; per step 512 + 1024 tensor cycles and, on each SM quarter, 1024
-// cycles of exponentials.  Up to 128 rows the kernel is bound by HBM; 256 rows
-// take two steps per tile, 1.6 us of MMAs alone.
+// copy bandwidth; per 128 rows 768 (S: 48 cycles per MMA at N = 64) + 1024 tensor
+// cycles and 1024 cycles of exponentials on each SM quarter.  Up to 128 rows the
+// kernel is bound by HBM; 256 rows take 3600 tensor cycles per tile, 1.9 us.
 //
 // Every wait is bounded: on a timeout the CTA raises PA_DEVERR_TIMEOUT, skips
 // what is left, lets its copies and MMAs drain, frees its tensor memory and
@@ -53,7 +54,7 @@ namespace {
 constexpr int TT_M = 128;               // rows of a stream: the MMA's M
 constexpr int TT_ROWS = 2 * TT_M;       // rows of a unit
 constexpr int TT_KT = 128;              // tokens of a K or V tile
-constexpr int TT_HT = TT_KT / 2;         // tokens of half a step's weights
+constexpr int TT_HT = TT_KT / 2;         // tokens of a step
 constexpr int TT_SLOTS = 5;             // ring slots (one K or V tile each)
 constexpr int TT_MASKS = 4;             // tiles whose token masks are kept
 constexpr int TT_SOFTMAX_WARPS = 8;     // warps 0-3: stream 0, 4-7: stream 1
@@ -77,20 +78,21 @@ struct TreeGeom {
     static constexpr int SLOT = TT_KT / 8 * GROUP;
     static constexpr int OFF_SLOTS = 2 * Q_TILE;
     static constexpr int BYTES = OFF_SLOTS + TT_SLOTS * SLOT;
-    // tensor memory columns: S / P of stream w at 128 w, O of stream w behind both
-    static constexpr int O_COL = 2 * TT_KT;
+    // tensor memory columns: S / P of stream w, buffer b at 128 w + 64 b, O of stream w
+    // behind them
+    static constexpr int O_COL = 4 * TT_HT;
     static_assert(O_COL + 2 * D <= TT_TMEM_COLS, "tensor memory");
     static_assert(TREE_WINDOWS_MAX * 4 <= TT_SLOTS * SLOT, "window sums fit the ring");
 };
 
-constexpr uint32_t TT_IDESC_S = umma_idesc_bf16(TT_M, TT_KT, 0, 0);
+constexpr uint32_t TT_IDESC_S = umma_idesc_bf16(TT_M, TT_HT, 0, 0);
 
 struct TreeShared {
     uint64_t full[TT_SLOTS], empty[TT_SLOTS];
     uint64_t masked[TT_MASKS];     // the tile's token mask is written
-    uint64_t s_full[2];            // S of the stream's step is in tensor memory
-    uint64_t p_full[2][2];         // [stream][half]: its weights are (128 arrivals)
-    uint64_t o_half[2], o_done[2]; // P.V of its first half, of both, has finished
+    uint64_t s_full[2][2];         // [stream][buffer]: S of the step is in tensor memory
+    uint64_t p_full[2][2];         // its weights are (128 arrivals)
+    uint64_t o_done[2][2];         // its P.V has finished
     uint64_t drain;
     alignas(16) uint32_t mask[TT_MASKS][TT_MASK_WORDS];
     uint32_t tmem;
@@ -126,7 +128,7 @@ __device__ __forceinline__ bool tt_wait(uint64_t* bar, uint32_t parity, volatile
 
 // A row's maximum was raised before chunk c of a step: scales what was summed with
 // the old one, O (when scale_o, once `bar` says that none of the stream's P.V runs)
-// and the weights of the chunk before c that were not handed over yet.  Out of
+// and the step's weights before chunk c.  Out of
 // line: it is rare, and the loop that calls it has to stay small for the
 // instruction caches (inlined, the softmax took 1.3 times as long).
 template <int D>
@@ -145,7 +147,7 @@ __device__ __noinline__ bool tt_rescale(uint32_t o_col, uint32_t s_col, float al
             tmem_store32(o_col + c0, o);
         }
     }
-    if (c & 1) {
+    if (c > 0) {
         tmem_await_stores();
         const uint32_t col = s_col + 32 * (c - 1);
         uint32_t pw[32];
@@ -183,12 +185,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         for (int i = 0; i < TT_MASKS; ++i) mbar_init(smem_u32(&sh.masked[i]), 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.s_full[i]), 1);
-            mbar_init(smem_u32(&sh.p_full[i][0]), TT_M);
-            mbar_init(smem_u32(&sh.p_full[i][1]), TT_M);
-            mbar_init(smem_u32(&sh.o_half[i]), 1);
-            mbar_init(smem_u32(&sh.o_done[i]), 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_u32(&sh.s_full[i >> 1][i & 1]), 1);
+            mbar_init(smem_u32(&sh.p_full[i >> 1][i & 1]), TT_M);
+            mbar_init(smem_u32(&sh.o_done[i >> 1][i & 1]), 1);
         }
         mbar_init(smem_u32(&sh.drain), 1);
         fence_barrier_init();
@@ -287,7 +287,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             return bars + static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(first) - reinterpret_cast<const uint8_t*>(&sh)) + 8u * i;
         };
         auto passed = [&](uint32_t bar, uint32_t parity) { return __all_sync(FULL_MASK, mbar_test_wait(bar, parity)); };
-        uint32_t base[2] = {0, 0};            // steps of each stream in earlier runs
+        uint32_t base = 0;                    // steps of each stream in earlier runs (the same for both)
         uint32_t k_slot = 0, k_phase = 0;     // ring slot of the next S's K and its phase
         uint32_t v_slot = 1, v_phase = 0;     // of the next P.V's V
         auto advance = [](uint32_t& slot, uint32_t& phase) {
@@ -299,62 +299,66 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         };
         while (walk.next(a, r)) {
             named_barrier_sync(TT_Q_BARRIER, TT_SOFTMAX + 32);   // Q written, O of the last run read
-            const bool two = __shfl_sync(FULL_MASK, r.per_tile, 0) == 2;   // every tile is a step of both streams
+            const bool two = __shfl_sync(FULL_MASK, r.per_tile, 0) == 2;   // every half is a step of both streams
             const int nt = __shfl_sync(FULL_MASK, r.t1 - r.t0, 0);
-            const int steps = two ? 2 * nt : nt;
+            const int last = two ? 3 : 1, steps = (last + 1) * nt;   // i & last == last: a tile's last step
             if (__any_sync(FULL_MASK, *abort_flag)) continue;
             tmem_fence_after_sync();
-            // Step i of the run: stream i % 2, its step base + i / 2.  S(i) needs its K
-            // and P.V(i - 2) done with the buffer; half h of P.V(i) needs its weights
-            // and its V.  Each goes in order; the barriers are tested without blocking.
-            int ns = 0, no = 0, h = 0;
+            // Step i of the run: stream i % 2, its step base + i / 2, whose parity is
+            // the buffer and whose half is the buffer's phase.  S(i) needs its K and
+            // P.V(i - 4) done with the buffer; P.V(i) needs its weights and its V.
+            // Each goes in order; the barriers are tested without blocking.
+            int ns = 0, no = 0;
             PollLimit limit;
             while (no < steps) {
                 bool progressed = false;
-                if (ns < steps && ns < no + 2 && passed(bar_at(sh.full, k_slot), k_phase)) {
-                    const uint32_t w = ns & 1, use = (w ? base[1] : base[0]) + (ns >> 1);
-                    if (ns < 2 || passed(bar_at(sh.o_done, w), (use & 1u) ^ 1u)) {
+                if (ns < steps && ns < no + 4 && passed(bar_at(sh.full, k_slot), k_phase)) {
+                    const uint32_t w = ns & 1, use = base + (ns >> 1), buf = use & 1u;
+                    if (ns < 4 || passed(bar_at(&sh.o_done[0][0], 2 * w + buf), ((use >> 1) & 1u) ^ 1u)) {
                         tmem_fence_after_sync();
+                        const uint32_t half = two ? (ns >> 1) & 1 : w;
                         const uint64_t qd = q_desc + (two && w ? Geo::Q_TILE >> 4 : 0);
-                        const uint64_t kd = k_desc + ((k_slot * Geo::SLOT) >> 4);
-                        const bool free_k = !two || w == 1;   // K's last reader
+                        const uint64_t kd = k_desc + ((k_slot * Geo::SLOT + half * (Geo::SLOT / 2)) >> 4);
+                        const uint32_t s_tmem = utmem + TT_KT * w + TT_HT * buf;
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks) {
                             // k-step inside a 128-byte row, 64-column half
                             constexpr int STEP = 32 >> 4;
-                            umma_bf16_elected(leader, utmem + TT_KT * w,
-                                              qd + (ks % 4) * STEP + (ks / 4) * (Geo::Q_HALF >> 4),
+                            umma_bf16_elected(leader, s_tmem, qd + (ks % 4) * STEP + (ks / 4) * (Geo::Q_HALF >> 4),
                                               kd + (ks % 4) * STEP + (ks / 4) * (1024 >> 4), TT_IDESC_S,
                                               ks > 0 ? 1u : 0u);
                         }
-                        umma_commit_elected(leader, bar_at(sh.s_full, w));
-                        if (free_k) umma_commit_elected(leader, bar_at(sh.empty, k_slot));
-                        if (free_k) advance(k_slot, k_phase);
+                        umma_commit_elected(leader, bar_at(&sh.s_full[0][0], 2 * w + buf));
+                        if ((ns & last) == last) {   // K's last reader
+                            umma_commit_elected(leader, bar_at(sh.empty, k_slot));
+                            advance(k_slot, k_phase);
+                        }
                         ++ns;
                         progressed = true;
                     }
                 }
                 if (no < ns) {
-                    const uint32_t w = no & 1, use = (w ? base[1] : base[0]) + (no >> 1);
-                    if (passed(bar_at(&sh.p_full[0][0], 2 * w + h), use & 1u) &&
-                        (h == 1 || passed(bar_at(sh.full, v_slot), v_phase))) {
+                    const uint32_t w = no & 1, use = base + (no >> 1), buf = use & 1u;
+                    if (passed(bar_at(&sh.p_full[0][0], 2 * w + buf), (use >> 1) & 1u) &&
+                        passed(bar_at(sh.full, v_slot), v_phase)) {
                         tmem_fence_after_sync();
-                        const uint64_t vd = v_desc + ((v_slot * Geo::SLOT + h * (Geo::SLOT / 2)) >> 4);
-                        const uint32_t p_tmem = utmem + TT_KT * w + TT_HT * h;
+                        const uint32_t half = two ? (no >> 1) & 1 : w;
+                        const uint64_t vd = v_desc + ((v_slot * Geo::SLOT + half * (Geo::SLOT / 2)) >> 4);
+                        const uint32_t p_tmem = utmem + TT_KT * w + TT_HT * buf;
                         const uint32_t o_tmem = utmem + Geo::O_COL + D * w;
-                        const uint32_t more = no >= 2 || h == 1 ? 1u : 0u;   // 0: the stream's first P.V of the run
-                        const bool free_v = h == 1 && (!two || w == 1);
+                        const uint32_t more = no >= 2 ? 1u : 0u;   // 0: the stream's first step of the run
 #pragma unroll
                         for (int kk = 0; kk < TT_HT / 16; ++kk) {
                             const uint32_t p = p_tmem + 32 * (kk / 2) + 8 * (kk % 2);
                             umma_bf16_tmem_a_elected(leader, o_tmem, p, vd + kk * (2 * Geo::GROUP >> 4), IDESC_O, kk > 0 ? 1u : more);
                             umma_bf16_tmem_a_elected(leader, o_tmem, p + 16, vd + kk * (2 * Geo::GROUP >> 4), IDESC_O, 1u);
                         }
-                        if (free_v) umma_commit_elected(leader, bar_at(sh.empty, v_slot));
-                        umma_commit_elected(leader, h == 0 ? bar_at(sh.o_half, w) : bar_at(sh.o_done, w));
-                        if (free_v) advance(v_slot, v_phase);
-                        no += h;
-                        h ^= 1;
+                        if ((no & last) == last) {
+                            umma_commit_elected(leader, bar_at(sh.empty, v_slot));
+                            advance(v_slot, v_phase);
+                        }
+                        umma_commit_elected(leader, bar_at(&sh.o_done[0][0], 2 * w + buf));
+                        ++no;
                         progressed = true;
                     }
                 }
@@ -368,8 +372,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     break;
                 }
             }
-            base[0] += (steps + 1) / 2;
-            base[1] += steps / 2;
+            base += steps / 2;
         }
         if (__any_sync(FULL_MASK, *abort_flag)) {   // every MMA issued so far
             umma_commit_elected(leader, smem_u32(&sh.drain));
@@ -384,7 +387,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // a zero scale would turn the masked -inf into NaN: the smallest normal
         // numbers leave every weight of a row at 1 just as well
         const float sl2 = a.scale_log2 == 0.f ? 1e-37f : a.scale_log2;
-        const uint32_t s_col = lanes + TT_KT * w;
         uint32_t ring = 0, tiles = 0, use = 0;    // ring position and tile of the run's start; the stream's steps
         while (walk.next(a, r)) {
             const bool two = r.per_tile == 2;
@@ -435,14 +437,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const int pre = r.ctx - r.n;
             float m = NEG_INF, l = 0.f;
             bool ok = __all_sync(FULL_MASK, !*abort_flag);
-            int taken = 0;                                  // the stream's steps in this run
-            for (int j = two ? 0 : w; j < nt && ok; j += two ? 1 : 2, ++taken, ++use) {
+            const int steps = two ? 2 * nt : nt;
+            for (int step = 0; step < steps && ok; ++step, ++use) {
+                const int j = two ? step >> 1 : step, h = two ? step & 1 : w;   // tile of the run, half of the tile
+                const uint32_t s_col = lanes + TT_KT * w + TT_HT * (use & 1u);
                 const uint32_t mi = (tiles + j) % TT_MASKS;
                 const uint32_t vg = ring + 2 * j + 1, vslot = vg % TT_SLOTS;
                 bool ready = tt_wait(&sh.masked[mi], ((tiles + j) / TT_MASKS) & 1u, abort_flag, a.dev_err);
-                const uint4 in4 = *reinterpret_cast<const uint4*>(sh.mask[mi]);
-                ready = ready && tt_wait(&sh.s_full[w], use & 1u, abort_flag, a.dev_err);
-                const bool all_in = (in4.x & in4.y & in4.z & in4.w) == 0xffffffffu;
+                const uint2 in = *reinterpret_cast<const uint2*>(&sh.mask[mi][2 * h]);
+                ready = ready && tt_wait(&sh.s_full[w][use & 1u], (use >> 1) & 1u, abort_flag, a.dev_err);
+                const bool all_in = (in.x & in.y) == 0xffffffffu;
                 if (!all_in) ready = ready && tt_wait(&sh.full[vslot], (vg / TT_SLOTS) & 1u, abort_flag, a.dev_err);
                 if (!__all_sync(FULL_MASK, ready)) {
                     ok = false;
@@ -450,36 +454,36 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 }
                 tmem_fence_after_sync();
                 // value rows of tokens that take no part may hold anything, NaN too:
-                // zero them, so that 0 * V stays 0 (two row tiles share the slot:
+                // zero them, so that 0 * V stays 0 (two row tiles share the half:
                 // stream 0's P.V comes first, and its warps do it)
                 if (!all_in && (!two || w == 0)) {
-                    uint8_t* vs = smem + Geo::OFF_SLOTS + vslot * Geo::SLOT;
-                    for (int i = row; i < TT_KT * NH * 8; i += TT_M) {
+                    uint8_t* vs = smem + Geo::OFF_SLOTS + vslot * Geo::SLOT + h * (Geo::SLOT / 2);
+                    for (int i = row; i < TT_HT * NH * 8; i += TT_M) {
                         const int tok = i / (NH * 8), ch = i % (NH * 8);
-                        if (!((sh.mask[mi][tok >> 5] >> (tok & 31)) & 1u))
+                        if (!(((tok < 32 ? in.x : in.y) >> (tok & 31)) & 1u))
                             *reinterpret_cast<uint4*>(vs + (tok / 8) * Geo::GROUP + (ch / 8) * 1024 + (tok % 8) * 128 + (ch % 8) * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                 }
-                const int p0 = (r.t0 + j) * TT_KT;
+                const int p0 = (r.t0 + j) * TT_KT + h * TT_HT;
                 if (busy) {
                     const float unseen = sl2 >= 0.f ? NEG_INF : INFINITY;   // times the scale: -inf
                     // One pass over S, 32 columns at a time with the next 32 under way:
                     // the running maximum is raised lazily (by more than
                     // RESCALE_THRESHOLD), and then everything before the chunk is scaled
-                    // down: the sum, O, and the weights of the step not handed over yet.
+                    // down: the sum, O, and the step's weights already written.
                     // That is rare after a run's first tiles; a pass of its own for the
                     // maximum took a quarter of the softmax's time.
-                    const bool every = all_in && p0 + TT_KT <= pre;   // every token seen by every row
+                    const bool every = all_in && p0 + TT_HT <= pre;   // every token seen by every row
                     f32x2 sum(0.f, 0.f);
                     uint32_t x[32];
                     tmem_issue32(s_col, x);
 #pragma unroll 1
-                    for (int c = 0; c < TT_MASK_WORDS; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         tmem_await32(x);
                         if (!every) {
-                            const uint32_t seen = sh.mask[mi][c] & tree_bits(mrow, a.mask_words32, p0 + 32 * c - pre);
+                            const uint32_t seen = (c ? in.y : in.x) & tree_bits(mrow, a.mask_words32, p0 + 32 * c - pre);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 if (!((seen >> k) & 1u)) x[k] = __float_as_uint(unseen);
@@ -509,12 +513,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                             if (up) m = mx;
                             l *= alpha;
                             sum = fma2(sum, f32x2(alpha, alpha), f32x2(0.f, 0.f));
-                            // O may be scaled only when none of this stream's P.V runs: before
-                            // this step's first half is handed over, or when that is done
-                            const bool late = c >= 2;
-                            ok &= tt_rescale<D>(o_col, s_col, alpha, c, taken > 0 || late,
-                                                late ? &sh.o_half[w] : &sh.o_done[w], late ? use & 1u : (use - 1) & 1u,
-                                                abort_flag, a.dev_err);
+                            // O may be scaled only when none of this stream's P.V runs
+                            ok &= tt_rescale<D>(o_col, s_col, alpha, c, step > 0, &sh.o_done[w][(use - 1) & 1u],
+                                                ((use - 1) >> 1) & 1u, abort_flag, a.dev_err);
                         }
                         // weights over S: 16 columns of hi = bf16(p), then 16 of lo = bf16(p - hi)
                         const float base = m == NEG_INF ? 0.f : m;
@@ -534,25 +535,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                             pw[16 + k] = pack_bf16(p, q);
                         }
                         sum = add2(sum, add2(part[0], part[1]));
-                        if (c + 1 < TT_MASK_WORDS) tmem_issue32(s_col + 32 * (c + 1), x);
+                        if (c == 0) tmem_issue32(s_col + 32, x);
                         tmem_issue_store32(s_col + 32 * c, pw);
-                        if (c & 1) {
-                            tmem_await_stores();
-                            tmem_fence_before_sync();
-                            mbar_arrive(smem_u32(&sh.p_full[w][c >> 1]));
-                        }
                     }
+                    tmem_await_stores();
                     float s0, s1;
                     sum.get(s0, s1);
                     l += s0 + s1;
-                } else {
-                    tmem_fence_before_sync();
-                    mbar_arrive(smem_u32(&sh.p_full[w][0]));
-                    mbar_arrive(smem_u32(&sh.p_full[w][1]));
                 }
+                tmem_fence_before_sync();
+                mbar_arrive(smem_u32(&sh.p_full[w][use & 1u]));
             }
             // the run's last P.V of this stream
-            if (ok && taken > 0) ok = tt_wait(&sh.o_done[w], (use - 1) & 1u, abort_flag, a.dev_err);
+            if (ok) ok = tt_wait(&sh.o_done[w][(use - 1) & 1u], ((use - 1) >> 1) & 1u, abort_flag, a.dev_err);
             tmem_fence_after_sync();
 
             // epilogue.  Two row tiles: every stream stores its own rows.  One:
@@ -588,7 +583,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     tmem_load32(first + c, o);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] *= f0;
-                    if (!two && nt > 1) {   // stream 1 took a tile
+                    if (!two) {
                         float o1[32];
                         tmem_load32(first + D + c, o1);
 #pragma unroll

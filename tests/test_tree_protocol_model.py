@@ -1,14 +1,15 @@
 """A model of the tensor-core tree attention kernel's barrier protocol, on the CPU.
 
-The kernel (csrc/tree_tc.cu) runs a loader warp, an MMA-issuing thread and two
-streams of softmax warps per CTA; the loader runs ahead over the CTA's runs, the
-others meet at a named barrier before each run.  As for the prefill kernel's
-model, whose barriers and clock this one uses: every run must complete under
-random timing, and no parity wait may look at a barrier that is two phases on.
-The token masks' ring, which has no "free" barrier of its own, is checked too:
-no mask may be overwritten before the stream that needs it has read it.
-Planted mistakes must be caught: a single mask instead of a ring, and an S issued
-before the P.V that reads the same buffer has finished.
+The kernel (csrc/tree_tc.cu) runs two loader warps (K, V), an MMA-issuing warp
+and two streams of softmax warps per CTA; the loaders run ahead over the CTA's
+runs, the others meet at a named barrier before each run.  As for the prefill
+kernel's model, whose barriers and clock this one uses: every run must complete
+under random timing, and no parity wait may look at a barrier that is two phases
+on.  The token masks' ring, which has no "free" barrier of its own, is checked
+too: no mask may be overwritten before the stream that needs it has read it, and
+O may be scaled only while none of the stream's P.V runs.  Planted mistakes must
+be caught: a single mask instead of a ring, and an S issued before the P.V that
+reads the same buffer has finished.
 """
 
 import random
@@ -28,115 +29,107 @@ class TreeSim(Sim):
         self.empty = [Barrier(f"empty[{i}]") for i in range(SLOTS)]
         self.masked = [Barrier(f"masked[{i}]") for i in range(masks)]
         self.mask = [None] * masks
-        one = lambda n: [Barrier(f"{n}[{w}]") for w in range(2)]  # noqa: E731
-        self.s_full, self.o_half, self.o_done = one("s_full"), one("o_half"), one("o_done")
-        self.p_full = [[Barrier(f"p_full[{w}][{h}]") for h in range(2)] for w in range(2)]
-        self.reading = [0, 0]     # P.V issued and not finished, per stream
+        pair = lambda n: [[Barrier(f"{n}[{w}][{b}]") for b in range(2)] for w in range(2)]  # noqa: E731
+        self.s_full, self.p_full, self.o_done = pair("s_full"), pair("p_full"), pair("o_done")
+        self.reading = [[0, 0], [0, 0]]     # P.V issued and not finished, per stream and buffer
 
-    def finish_pv(self, w, bar):
+    def finish_pv(self, w, b):
         def done():
-            self.reading[w] -= 1
-            bar.arrive()
+            self.reading[w][b] -= 1
+            self.o_done[w][b].arrive()
         at = max(self.mma_free_at, self.now) + 1
         self.seq += 1
         self.events.append((at, self.seq, done))
 
 
-def loader(sim, runs):
-    ring = tile = 0
+def loader(sim, runs, v):
+    ring, tile = v, 0
     for nt, two in runs:
         for _ in range(nt):
-            for v in range(2):
-                slot = ring % SLOTS
-                if ring >= SLOTS:
-                    while not sim.empty[slot].passed(ring // SLOTS - 1):
-                        yield
-                if v == 0:
-                    sim.mask[tile % sim.masks] = tile
-                    sim.masked[tile % sim.masks].arrive()
-                yield from sim.pause(2)
-                sim.full[slot].arrive(tx=64)
-                sim.copy(sim.full[slot], 64)
-                ring += 1
+            slot = ring % SLOTS
+            if ring >= SLOTS:
+                while not sim.empty[slot].passed(ring // SLOTS - 1):
+                    yield
+            yield from sim.pause(2)
+            sim.full[slot].arrive(tx=64)
+            sim.copy(sim.full[slot], 64)
+            if v == 0:
+                yield from sim.pause(1)
+                sim.mask[tile % sim.masks] = tile
+                sim.masked[tile % sim.masks].arrive()
+            ring += 2
             tile += 1
 
 
 def mma(sim, runs):
-    ring, base = 0, [0, 0]
+    ring = base = 0
     for nt, two in runs:
         yield "sync"
-        steps = 2 * nt if two else nt
-        ns = no = h = 0
-        k_at = lambda i: ring + 2 * (i >> 1 if two else i)  # noqa: E731
-        use = lambda i: base[i & 1] + (i >> 1)  # noqa: E731
+        per = 4 if two else 2
+        steps = per * nt
+        ns = no = 0
+        k_at = lambda i: ring + 2 * (i // per)  # noqa: E731
+        use = lambda i: base + (i >> 1)  # noqa: E731
         landed = lambda g: sim.full[g % SLOTS].passed(g // SLOTS)  # noqa: E731
         while no < steps:
-            w = ns & 1
-            if ns < steps and ns < no + 2 + sim.early_s and landed(k_at(ns)) and \
-                    (ns < 2 or sim.early_s or sim.o_done[w].passed(use(ns) - 1)):
-                if sim.reading[w]:
+            w, u = ns & 1, use(ns)
+            if ns < steps and ns < no + 4 + sim.early_s and landed(k_at(ns)) and \
+                    (ns < 4 or sim.early_s or sim.o_done[w][u & 1].passed((u >> 1) - 1)):
+                if sim.reading[w][u & 1]:
                     raise AssertionError("S issued over weights that a P.V still reads")
-                sim.mma(5)
-                sim.commit(sim.s_full[w])
-                if not two or w:
+                sim.mma(4)
+                sim.commit(sim.s_full[w][u & 1])
+                if ns % per == per - 1:
                     sim.commit(sim.empty[k_at(ns) % SLOTS])
                 ns += 1
-            w = no & 1
-            if no < ns and sim.p_full[w][h].passed(use(no)) and (h or landed(k_at(no) + 1)):
+            w, u = no & 1, use(no)
+            if no < ns and sim.p_full[w][u & 1].passed(u >> 1) and landed(k_at(no) + 1):
                 sim.mma(5)
-                sim.reading[w] += 1
-                if h and (not two or w):
+                sim.reading[w][u & 1] += 1
+                if no % per == per - 1:
                     sim.commit(sim.empty[(k_at(no) + 1) % SLOTS])
-                sim.finish_pv(w, sim.o_done[w] if h else sim.o_half[w])
-                no += h
-                h ^= 1
+                sim.finish_pv(w, u & 1)
+                no += 1
             yield
             yield from sim.pause(2)
         ring += 2 * nt
-        base[0] += (steps + 1) // 2
-        base[1] += steps // 2
+        base += steps // 2
 
 
 def softmax(sim, runs, w):
     ring = tiles = use = 0
     for nt, two in runs:
         yield "sync"
-        taken = 0
-        for j in range(0 if two else w, nt, 1 if two else 2):
+        for k in range(2 * nt if two else nt):
+            j = k >> 1 if two else k
             t = tiles + j
             while not sim.masked[t % sim.masks].passed(t // sim.masks):
                 yield
             if sim.mask[t % sim.masks] != t:
                 raise AssertionError("a token mask was overwritten before it was read")
-            while not sim.s_full[w].passed(use):
+            while not sim.s_full[w][use & 1].passed(use >> 1):
                 yield
             if sim.rng.random() < 0.3:          # tokens that take no part: V is zeroed
                 g = ring + 2 * j + 1
                 while not sim.full[g % SLOTS].passed(g // SLOTS):
                     yield
-            for h in range(2):
-                if (h or taken) and sim.rng.random() < 0.3:   # O scaled: none of its P.V may run
-                    bar, phase = (sim.o_half[w], use) if h else (sim.o_done[w], use - 1)
-                    while not bar.passed(phase):
-                        yield
-                    if sim.reading[w]:
-                        raise AssertionError("O scaled while a P.V adds to it")
-                yield from sim.pause(5)
-                if sim.mask[t % sim.masks] != t:
-                    raise AssertionError("a token mask was overwritten before it was read")
-                sim.p_full[w][h].arrive()
+            if k and sim.rng.random() < 0.3:    # O scaled
+                while not sim.o_done[w][(use - 1) & 1].passed((use - 1) >> 1):
+                    yield
+                if any(sim.reading[w]):
+                    raise AssertionError("O scaled while a P.V adds to it")
+            yield from sim.pause(8)
+            sim.p_full[w][use & 1].arrive()
             use += 1
-            taken += 1
-        if taken:
-            while not sim.o_done[w].passed(use - 1):
-                yield
+        while not sim.o_done[w][(use - 1) & 1].passed((use - 1) >> 1):
+            yield
         ring += 2 * nt
         tiles += nt
 
 
 def run(runs, seed, max_steps=200000, **planted):
     sim = TreeSim(seed, **planted)
-    roles = {"load": loader(sim, runs), "mma": mma(sim, runs), "s0": softmax(sim, runs, 0), "s1": softmax(sim, runs, 1)}
+    roles = {"load k": loader(sim, runs, 0), "load v": loader(sim, runs, 1), "mma": mma(sim, runs), "s0": softmax(sim, runs, 0), "s1": softmax(sim, runs, 1)}
     at_sync, finished = set(), set()
     for _ in range(max_steps):
         if len(finished) == len(roles):
@@ -155,7 +148,7 @@ def run(runs, seed, max_steps=200000, **planted):
                 if got == "sync":
                     at_sync.add(name)
                     break
-        if at_sync == {"mma", "s0", "s1"}:       # the loader does not take part
+        if at_sync == {"mma", "s0", "s1"}:       # the loaders do not take part
             at_sync.clear()
         if sim.events:
             sim.events.sort(key=lambda e: e[:2])
