@@ -251,8 +251,8 @@ int launch_tree_simt(const TreeArgs& a, int ctas, cudaStream_t st) {
 // the grid joins it.
 // ---------------------------------------------------------------------------
 
-constexpr int TJ_THREADS = 128;
-constexpr int TJ_ROWS = 32;   // rows per CTA
+constexpr int TJ_THREADS = 256;
+constexpr int TJ_ROWS = 16;   // rows per CTA: two float4 per thread at d = 128, so that all loads go out at once
 
 template <int D>
 __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const TreeArgs a, int ctas) {
@@ -294,38 +294,68 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const TreeArgs a,
     }
     __syncthreads();
     const int parts = s_parts;
-    if (threadIdx.x < here) {
-        const int row = row0 + threadIdx.x;
+    // coefficients: half a warp per row, a lane per partial
+    const int sub = threadIdx.x & 15, rr = threadIdx.x >> 4;
+    if (rr < here) {
+        const size_t row = row0 + rr;
         float M = NEG_INF, L = 0.f;
-        for (int p = 0; p < parts; ++p) M = fmaxf(M, a.part_ml[static_cast<size_t>(s_slot[p]) * a.part_rows + row].x);
-        for (int p = 0; p < parts; ++p) {
-            const float2 ml = a.part_ml[static_cast<size_t>(s_slot[p]) * a.part_rows + row];
+        float2 ml0 = make_float2(NEG_INF, 0.f);
+        if (sub < parts) ml0 = a.part_ml[static_cast<size_t>(s_slot[sub]) * a.part_rows + row];
+        M = ml0.x;
+        for (int p = sub + 16; p < parts; p += 16)
+            M = fmaxf(M, a.part_ml[static_cast<size_t>(s_slot[p]) * a.part_rows + row].x);
+        const unsigned half = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(half, M, off));
+        for (int p = sub; p < parts; p += 16) {
+            const float2 ml = p == sub ? ml0 : a.part_ml[static_cast<size_t>(s_slot[p]) * a.part_rows + row];
             const float e = M == NEG_INF ? 0.f : exp2_approx(ml.x - M);
-            s_coef[threadIdx.x][p] = e;
+            s_coef[rr][p] = e;
             L = fmaf(e, ml.y, L);
         }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) L += __shfl_xor_sync(half, L, off);
         const float inv = L > 0.f ? 1.f / L : 0.f;
-        for (int p = 0; p < parts; ++p) s_coef[threadIdx.x][p] *= inv;
+        for (int p = sub; p < parts; p += 16) s_coef[rr][p] *= inv;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < TJ_ROWS * (D / 4); i += TJ_THREADS) {
-        const int rr = i % TJ_ROWS, c4 = i / TJ_ROWS;
-        if (rr >= here) continue;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < parts; ++p) {
-            const float e = s_coef[rr][p];
-            const float4 v = reinterpret_cast<const float4*>(tree_part(a, s_slot[p], D))[c4 * a.part_rows + row0 + rr];
-            o.x = fmaf(e, v.x, o.x);
-            o.y = fmaf(e, v.y, o.y);
-            o.z = fmaf(e, v.z, o.z);
-            o.w = fmaf(e, v.w, o.w);
+    constexpr int ITEMS = TJ_ROWS * (D / 4) / TJ_THREADS, U = 4;
+    const int i0 = threadIdx.x % TJ_ROWS;   // row, fastest over the threads: the partials' order
+    if (i0 >= here) return;
+    float4 o[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < parts; p0 += U) {
+        float4 v[U][ITEMS];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k)
+                if (p0 + u < parts)
+                    v[u][k] = reinterpret_cast<const float4*>(tree_part(a, s_slot[p0 + u], D))
+                        [(threadIdx.x / TJ_ROWS + k * (TJ_THREADS / TJ_ROWS)) * a.part_rows + row0 + i0];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (p0 + u >= parts) break;
+            const float e = s_coef[i0][p0 + u];
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                o[k].x = fmaf(e, v[u][k].x, o[k].x);
+                o[k].y = fmaf(e, v[u][k].y, o[k].y);
+                o[k].z = fmaf(e, v[u][k].z, o[k].z);
+                o[k].w = fmaf(e, v[u][k].w, o[k].w);
+            }
         }
-        const size_t at = tree_out_row(a, r.first, r.kvh, r.row0 + row0 + rr) * D + 4 * c4;
+    }
+    const size_t at = tree_out_row(a, r.first, r.kvh, r.row0 + row0 + i0) * D;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const size_t col = at + 4 * (threadIdx.x / TJ_ROWS + k * (TJ_THREADS / TJ_ROWS));
         if (a.out_f32)
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = o;
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + col) = o[k];
         else
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
-                make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + col) =
+                make_uint2(pack_bf16(o[k].x, o[k].y), pack_bf16(o[k].z, o[k].w));
     }
 }
 

@@ -244,10 +244,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const uint32_t bar = smem_u32(&sh.full[slot]);
                 mbar_arrive_expect_tx_elected(leader, bar, bytes);
                 const uint32_t dst = slots + slot * Geo::SLOT;
-                for (int i = 0; i < per; ++i) {
-                    const int at = __shfl_sync(FULL_MASK, group, i);
-                    if ((valid >> i) & 1u)
-                        tma_load_group_elected(leader, dst + i * (B / 8) * Geo::GROUP, map, bar, at);
+                for (int i = 0; i < per; i += 4) {   // four at a time: their shuffles overlap
+                    int at[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) at[u] = __shfl_sync(FULL_MASK, group, i + u);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        tma_load_group_elected(leader & (valid >> (i + u)), dst + (i + u) * (B / 8) * Geo::GROUP, map, bar, at[u]);
                 }
                 if (!is_v) {
                     // tokens of the tile that take part: in the context and in a valid
@@ -309,10 +312,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             // P.V(i - 4) done with the buffer; P.V(i) needs its weights and its V.
             // Each goes in order; the barriers are tested without blocking.
             int ns = 0, no = 0;
+            bool k_here = false, v_here = false;   // the slot's copy was seen to have landed
             PollLimit limit;
             while (no < steps) {
                 bool progressed = false;
-                if (ns < steps && ns < no + 4 && passed(bar_at(sh.full, k_slot), k_phase)) {
+                if (ns < steps && ns < no + 4 && (k_here || (k_here = passed(bar_at(sh.full, k_slot), k_phase)))) {
                     const uint32_t w = ns & 1, use = base + (ns >> 1), buf = use & 1u;
                     if (ns < 4 || passed(bar_at(&sh.o_done[0][0], 2 * w + buf), ((use >> 1) & 1u) ^ 1u)) {
                         tmem_fence_after_sync();
@@ -332,6 +336,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         if ((ns & last) == last) {   // K's last reader
                             umma_commit_elected(leader, bar_at(sh.empty, k_slot));
                             advance(k_slot, k_phase);
+                            k_here = false;
                         }
                         ++ns;
                         progressed = true;
@@ -340,7 +345,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 if (no < ns) {
                     const uint32_t w = no & 1, use = base + (no >> 1), buf = use & 1u;
                     if (passed(bar_at(&sh.p_full[0][0], 2 * w + buf), (use >> 1) & 1u) &&
-                        passed(bar_at(sh.full, v_slot), v_phase)) {
+                        (v_here || (v_here = passed(bar_at(sh.full, v_slot), v_phase)))) {
                         tmem_fence_after_sync();
                         const uint32_t half = two ? (no >> 1) & 1 : w;
                         const uint64_t vd = v_desc + ((v_slot * Geo::SLOT + half * (Geo::SLOT / 2)) >> 4);
@@ -356,6 +361,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         if ((no & last) == last) {
                             umma_commit_elected(leader, bar_at(sh.empty, v_slot));
                             advance(v_slot, v_phase);
+                            v_here = false;
                         }
                         umma_commit_elected(leader, bar_at(&sh.o_done[0][0], 2 * w + buf));
                         ++no;
@@ -364,7 +370,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 }
                 if (progressed) {
                     limit = PollLimit();
-                } else if (__any_sync(FULL_MASK, *abort_flag)) {
+                    continue;
+                }
+                // Nothing to issue: sleep on what most likely comes next (the weights of
+                // the step in turn, or K), but not long, since anything may.  Polling
+                // without a pause takes issue slots from the softmax warps beside it.
+                if (no < ns) {
+                    const uint32_t w = no & 1, use = base + (no >> 1);
+                    mbar_try_wait_for(bar_at(&sh.p_full[0][0], 2 * w + (use & 1u)), (use >> 1) & 1u, 200);
+                } else {
+                    mbar_try_wait_for(bar_at(sh.full, k_slot), k_phase, 200);
+                }
+                __syncwarp();
+                if (__any_sync(FULL_MASK, *abort_flag)) {
                     break;
                 } else if (__any_sync(FULL_MASK, limit.out())) {
                     *abort_flag = 1;
