@@ -27,16 +27,19 @@ namespace pa {
 // one ordered pass writes the positions whose key is above it and the first
 // ones equal to it.
 //
-// A row is split over a cluster of CTAs, each with a contiguous segment; a
-// pass adds the segments' histograms through distributed shared memory, so
-// every CTA knows the digit without another launch.  The segment's keys stay
-// in shared memory over the passes (one read of the totals); only rows whose
-// segments do not fit are read again (from L2).
+// A row is split over a cluster of CTAs, each with a contiguous segment.  In a pass
+// every CTA counts its segment's digits in shared memory and adds its counts to
+// the leader's through distributed shared memory (adds return nothing, so nobody
+// waits for them); the leader finds the digit and writes it to every CTA.  Reading
+// all CTAs' counts from every CTA instead took most of a pass.  The segment's keys
+// stay in shared memory over the passes where that leaves the whole launch
+// resident; else they are read again, from L2.
 // ---------------------------------------------------------------------------
 
 constexpr int SEL_THREADS = 512;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_BINS = 2048;
+constexpr int SEL_PER = SEL_BINS / SEL_THREADS;   // bins per thread
 constexpr int SEL_MAX_CLUSTER = 8;
 constexpr int SEL_SMEM_KEYS = 48 * 1024;   // keys a CTA can hold (192 KB)
 
@@ -59,19 +62,49 @@ __device__ __forceinline__ uint32_t total_key(float w) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// Keys i .. i + 3 of a segment (i a multiple of 4); those past `len` are 0, the
+// key of no total.
+struct SegmentKeys {
+    const float* w;
+    uint32_t* cache;   // null: not held
+    int len;
+    bool vec;          // w is 16-byte aligned
+    __device__ __forceinline__ uint4 load(int i) const {
+        float v[4];
+        if (vec && i + 4 <= len) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(w + i));
+            v[0] = f.x;
+            v[1] = f.y;
+            v[2] = f.z;
+            v[3] = f.w;
+            return make_uint4(total_key(v[0]), total_key(v[1]), total_key(v[2]), total_key(v[3]));
+        }
+        uint32_t k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = i + j < len ? total_key(__ldg(w + i + j)) : 0u;
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    }
+    __device__ __forceinline__ uint4 get(int i) const {
+        return cache != nullptr ? *reinterpret_cast<const uint4*>(cache + i) : load(i);
+    }
+};
+
 __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a) {
-    extern __shared__ uint32_t s_keys[];
-    __shared__ uint32_t hist[SEL_BINS];
+    extern __shared__ __align__(16) uint32_t s_keys[];
+    __shared__ uint32_t hist[2][SEL_BINS];   // by pass parity: one is cleared while the other is in use
     __shared__ int s_scan[33];
-    __shared__ uint32_t s_digit, s_above;
-    __shared__ int2 s_warp[SEL_WARPS];   // (above, equal) of each warp's sub-segment
-    __shared__ int2 s_cta;               // and of the segment, read by the cluster
+    __shared__ uint32_t s_found[2];          // the pass's digit, and how many keys lie above it
+    __shared__ int2 s_warp[SEL_WARPS];       // (above, equal) of each warp's sub-segment
+    __shared__ int2 s_cta;                   // and of the segment, read by the cluster
+    __shared__ int2 s_base;                  // and of the segments before it
     cg::cluster_group cluster = cg::this_cluster();
     const int CL = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
     const int row = blockIdx.x / CL;
     const int s = row / a.num_kv_heads;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+#pragma unroll
+    for (int i = 0; i < 2 * SEL_PER; ++i) hist[i / SEL_PER][(i % SEL_PER) * SEL_THREADS + tid] = 0;
     pdl_wait();
     pdl_launch_dependents();
 
@@ -95,13 +128,17 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
 
     const int seg = ((m + CL - 1) / CL + 31) & ~31;
     const int lo = min(m, rank * seg), len = min(m, lo + seg) - lo;
-    const float* w = a.weights + static_cast<size_t>(row) * a.weights_stride + lo;
-    const bool cached = seg <= a.cached_keys;
-    auto key_at = [&](int i) { return cached ? s_keys[i] : total_key(__ldg(w + i)); };
-    if (cached) {
-        for (int i = tid; i < len; i += SEL_THREADS) s_keys[i] = total_key(__ldg(w + i));
-        __syncthreads();
+    SegmentKeys keys;
+    keys.w = a.weights + static_cast<size_t>(row) * a.weights_stride + lo;
+    keys.len = len;
+    keys.vec = (reinterpret_cast<uintptr_t>(keys.w) & 15u) == 0;
+    keys.cache = nullptr;
+    if (seg <= a.cached_keys) {
+#pragma unroll 4
+        for (int i = 4 * tid; i < len; i += 4 * SEL_THREADS) *reinterpret_cast<uint4*>(s_keys + i) = keys.load(i);
+        keys.cache = s_keys;
     }
+    cluster.sync();            // cleared counts (the leader's before anybody adds), own keys
 
     uint32_t prefix = 0;       // digits found so far
     uint32_t want = k;         // rank of the sought key among those with the prefix
@@ -112,56 +149,88 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
         const int hi_shift = shift;
         shift -= bits;
         const uint32_t mask = (1u << bits) - 1u;
-        for (int i = tid; i < SEL_BINS; i += SEL_THREADS) hist[i] = 0;
-        __syncthreads();
-        for (int i0 = 0; i0 < len; i0 += SEL_THREADS) {
-            const int i = i0 + tid;
-            const uint32_t key = i < len ? key_at(i) : 0u;
-            const bool in = i < len && (pass == 0 || (key >> hi_shift) == prefix);
-            const uint32_t d = (key >> shift) & mask;
-            // totals that repeat (zeros above all) would add to one bin 32 times over
-            const unsigned live = __ballot_sync(FULL_MASK, in);
-            if (live == 0u) continue;
-            const uint32_t first = __shfl_sync(FULL_MASK, d, __ffs(live) - 1);
-            const unsigned same = __ballot_sync(FULL_MASK, in && d == first);
-            if (lane == __ffs(live) - 1) atomicAdd(&hist[first], __popc(same));
-            if (in && d != first) atomicAdd(&hist[d], 1u);
-        }
-        cluster.sync();        // every segment's histogram is complete
-        // thread t owns bins [t * PER, (t + 1) * PER) counted from the top
-        constexpr int PER = SEL_BINS / SEL_THREADS;
-        uint32_t cnt[PER], sum = 0;
+        uint32_t* h = hist[pass & 1];
+#pragma unroll 2
+        for (int i = 4 * tid; i < len; i += 4 * SEL_THREADS) {
+            const uint4 k4 = keys.get(i);
+            const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+            // neighbours with one digit (zeros above all) add once
+            uint32_t at = 0, count = 0;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            cnt[j] = 0;
-            const int bin = SEL_BINS - 1 - (tid * PER + j);
-            for (int c = 0; c < CL; ++c) cnt[j] += *cluster.map_shared_rank(&hist[bin], c);
-            sum += cnt[j];
-        }
-        int total;
-        uint32_t before = static_cast<uint32_t>(cta_exclusive_scan(static_cast<int>(sum), &total, s_scan));
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            if (before < want && want <= before + cnt[j]) {   // exactly one thread and bin
-                s_digit = SEL_BINS - 1 - (tid * PER + j);
-                s_above = before;
+            for (int j = 0; j < 4; ++j) {
+                const bool in = i + j < len && (pass == 0 || (kk[j] >> hi_shift) == prefix);
+                if (!in) continue;
+                const uint32_t d = (kk[j] >> shift) & mask;
+                if (count != 0 && d != at) {
+                    atomicAdd(&h[at], count);
+                    count = 0;
+                }
+                at = d;
+                ++count;
             }
-            before += cnt[j];
+            if (count != 0) atomicAdd(&h[at], count);
         }
-        cluster.sync();        // digit known; no CTA still reads another's histogram
-        prefix = (prefix << bits) | s_digit;
-        want -= s_above;
+        if (CL > 1) {
+            __syncthreads();
+            if (rank != 0) {
+                uint32_t* lead = cluster.map_shared_rank(h, 0);
+#pragma unroll
+                for (int j = 0; j < SEL_PER; ++j) {
+                    const uint32_t c = h[j * SEL_THREADS + tid];
+                    if (c != 0) atomicAdd(lead + j * SEL_THREADS + tid, c);
+                }
+            }
+        }
+        cluster.sync();        // the leader has every segment's counts
+        if (rank == 0) {
+            // thread t owns SEL_PER bins counted from the top
+            uint32_t cnt[SEL_PER], sum = 0;
+#pragma unroll
+            for (int j = 0; j < SEL_PER; ++j) {
+                cnt[j] = h[SEL_BINS - 1 - (tid * SEL_PER + j)];
+                sum += cnt[j];
+            }
+            int total;
+            uint32_t before = static_cast<uint32_t>(cta_exclusive_scan(static_cast<int>(sum), &total, s_scan));
+#pragma unroll
+            for (int j = 0; j < SEL_PER; ++j) {
+                if (before < want && want <= before + cnt[j]) {   // exactly one thread and bin
+                    for (int c = 0; c < CL; ++c) {
+                        uint32_t* to = cluster.map_shared_rank(s_found, c);
+                        to[0] = SEL_BINS - 1 - (tid * SEL_PER + j);
+                        to[1] = before;
+                    }
+                }
+                before += cnt[j];
+            }
+            __syncthreads();   // counts read by all before they are cleared
+        }
+#pragma unroll
+        for (int j = 0; j < SEL_PER; ++j) h[j * SEL_THREADS + tid] = 0;   // for the pass after the next
+        cluster.sync();        // the digit is known
+        prefix = (prefix << bits) | s_found[0];
+        want -= s_found[1];
     }
     // want = how many of the keys equal to prefix stay, the first ones by position
 
-    // warp w takes a contiguous part of the segment
-    const int part = ((len + SEL_WARPS - 1) / SEL_WARPS + 31) & ~31;
+    // warp w takes a contiguous part of the segment, a lane four keys at a time
+    const int part = ((len + SEL_WARPS - 1) / SEL_WARPS + 127) & ~127;
     const int w0 = min(len, warp * part), w1 = min(len, w0 + part);
+    auto tell = [&](const uint4& k4, int i, int (&up)[4], int (&eq)[4]) {
+        const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            up[j] = i + j < w1 && kk[j] > prefix;
+            eq[j] = i + j < w1 && kk[j] == prefix;
+        }
+    };
     int above = 0, equal = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t key = key_at(i);
-        above += key > prefix;
-        equal += key == prefix;
+#pragma unroll 2
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+        int up[4], eq[4];
+        tell(keys.get(i), i, up, eq);
+        above += up[0] + up[1] + up[2] + up[3];
+        equal += eq[0] + eq[1] + eq[2] + eq[3];
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -170,37 +239,44 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
     }
     if (lane == 0) s_warp[warp] = make_int2(above, equal);
     __syncthreads();
-    if (tid == 0) {
-        int2 t = make_int2(0, 0);
-        for (int i = 0; i < SEL_WARPS; ++i) {
-            const int2 x = s_warp[i];
-            s_warp[i] = t;
-            t.x += x.x;
-            t.y += x.y;
-        }
-        s_cta = t;
+    if (warp == 0) {
+        const int2 x = lane < SEL_WARPS ? s_warp[lane] : make_int2(0, 0);
+        const int ix = warp_inclusive_scan(x.x), iy = warp_inclusive_scan(x.y);
+        if (lane < SEL_WARPS) s_warp[lane] = make_int2(ix - x.x, iy - x.y);
+        if (lane == 31) s_cta = make_int2(ix, iy);
     }
     cluster.sync();
-    int base_above = s_warp[warp].x, base_equal = s_warp[warp].y;
-    for (int c = 0; c < rank; ++c) {
-        const int2 t = *cluster.map_shared_rank(&s_cta, c);
-        base_above += t.x;
-        base_equal += t.y;
+    if (warp == 0) {
+        int2 x = make_int2(0, 0);
+        if (lane < rank) x = *cluster.map_shared_rank(&s_cta, lane);
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) {
+            x.x += __shfl_xor_sync(FULL_MASK, x.x, off);
+            x.y += __shfl_xor_sync(FULL_MASK, x.y, off);
+        }
+        if (lane == 0) s_base = x;
     }
+    cluster.sync();   // and s_cta is no longer read by the cluster
+    int base_above = s_warp[warp].x + s_base.x, base_equal = s_warp[warp].y + s_base.y;
     const int quota = static_cast<int>(want);
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t key = i < w1 ? key_at(i) : 0u;
-        const bool up = i < w1 && key > prefix, eq = i < w1 && key == prefix;
-        const unsigned bu = __ballot_sync(FULL_MASK, up), be = __ballot_sync(FULL_MASK, eq);
-        const unsigned below = (1u << lane) - 1u;
-        const int eq_before = base_equal + __popc(be & below);
-        if (up || (eq && eq_before < quota))
-            out[base_above + __popc(bu & below) + min(eq_before, quota)] = lo + i;
-        base_above += __popc(bu);
-        base_equal += __popc(be);
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        int up[4] = {0, 0, 0, 0}, eq[4] = {0, 0, 0, 0};
+        if (i < w1) tell(keys.get(i), i, up, eq);
+        const int nu = up[0] + up[1] + up[2] + up[3], ne = eq[0] + eq[1] + eq[2] + eq[3];
+        // both counts of a lane in one scan: at most 128 each
+        const int inc = warp_inclusive_scan(nu | (ne << 16));
+        int bu = base_above + (inc & 0xffff) - nu, be = base_equal + (inc >> 16) - ne;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (up[j] || (eq[j] && be < quota)) out[bu + min(be, quota)] = lo + i + j;
+            bu += up[j];
+            be += eq[j];
+        }
+        const int all = __shfl_sync(FULL_MASK, inc, 31);
+        base_above += all & 0xffff;
+        base_equal += all >> 16;
     }
-    cluster.sync();   // s_cta is read by the cluster until here
 }
 
 // ---------------------------------------------------------------------------
@@ -211,11 +287,16 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
 // enough that, within one (s, h), chunk c of destinations is written after the
 // sources of chunks 0 .. c were read: later chunks' sources lie above every
 // destination of chunk c.  One CTA walks the chunks of one (s, h) in order,
-// loads running ahead of the stores; other CTAs take the other pool and other
-// 16-byte columns of the same rows, which never meet.
+// loads running ahead of the stores; other CTAs take the other pool, other 16-byte
+// columns of the same rows, and the totals, which never meet.
+//
+// Bound by HBM when there are many walks, by the round trips of a chunk when there
+// are few (positions, table entries and rows are fetched one, two and three stages
+// ahead of the store): then a CTA has 1024 threads, so that a chunk is four times
+// as long.
 // ---------------------------------------------------------------------------
 
-constexpr int CMP_THREADS = 256;
+constexpr int CMP_THREADS = 256, CMP_THREADS_FEW = 1024;
 constexpr int CMP_ROWS = 4;   // rows per thread and chunk
 
 struct CompactArgs {
@@ -234,90 +315,116 @@ struct CompactArgs {
     int num_blocks, block_size, log2_block, row_vecs;
     int log2_vecs;            // 16-byte columns per CTA: 1 << log2_vecs
     int slices;               // CTAs along a row: row_vecs >> log2_vecs
+    int walks;                // CTAs per (s, h): 2 pools x slices, and one for the totals if there are any
 };
 
-__global__ void __launch_bounds__(CMP_THREADS) compact_kernel(const CompactArgs a) {
+// What a walk knows of its (s, h).
+struct CompactRow {
+    const int32_t* keep;
+    const int32_t* src_table;
+    const int32_t* dst_table;
+    int n, start;
+};
+
+// Position keep[j], or -1 when it may not move (past the row's end: silently).
+__device__ __forceinline__ int compact_source(const CompactArgs& a, const CompactRow& r, int j, int pos, bool report) {
+    if (j >= r.n) return -1;
+    const long long d = static_cast<long long>(r.start) + j;
+    if (pos < d || pos >= (static_cast<long long>(a.src_blocks) << a.log2_block) ||
+        d >= (static_cast<long long>(a.dst_blocks) << a.log2_block)) {
+        if (report) flag_error(a.dev_err, PA_DEVERR_COPY);
+        return -1;
+    }
+    return pos;
+}
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kernel(const CompactArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    // blockIdx.x = ((s * Hkv + h) * 2 + pool) * slices + slice
-    int b = blockIdx.x;
-    const int slice = b % a.slices;
-    b /= a.slices;
-    const int which = b & 1;
-    const int row = b >> 1, s = row / a.num_kv_heads, h = row - s * a.num_kv_heads;
+    // blockIdx.x = (s * Hkv + h) * walks + walk
+    const int row = blockIdx.x / a.walks, walk = blockIdx.x - row * a.walks;
+    const int s = row / a.num_kv_heads, h = row - s * a.num_kv_heads;
     const int raw = a.keep_lens[s];
-    const int n = clamp_context(raw, a.keep_stride);
-    const int start = a.starts != nullptr ? a.starts[s] : 0;
-    const bool lead = slice == 0 && which == 0;   // the CTA that reports and moves the totals
-    if (lead && threadIdx.x == 0 && h == 0 && (raw != n || start < 0)) flag_error(a.dev_err, PA_DEVERR_CONTEXT);
-    if (start < 0 || n == 0) return;
+    CompactRow r;
+    r.n = clamp_context(raw, a.keep_stride);
+    r.start = a.starts != nullptr ? a.starts[s] : 0;
+    if (walk == 0 && threadIdx.x == 0 && h == 0 && (raw != r.n || r.start < 0)) flag_error(a.dev_err, PA_DEVERR_CONTEXT);
+    if (r.start < 0 || r.n == 0) return;
+    r.keep = a.keep + (static_cast<size_t>(s) * a.keep_heads + (a.keep_heads > 1 ? h : 0)) * a.keep_stride;
+    r.src_table = a.src_tables + static_cast<size_t>(s) * a.src_blocks;
+    r.dst_table = a.dst_tables + static_cast<size_t>(s) * a.dst_blocks;
 
+    if (walk == 2 * a.slices) {   // the totals: a thread per position
+        const float* in = a.w_in + static_cast<size_t>(row) * a.w_stride;
+        float* out = a.w_out + static_cast<size_t>(row) * a.w_stride;
+        constexpr int CHUNK = THREADS * CMP_ROWS;
+        for (int j0 = 0; j0 < r.n; j0 += CHUNK) {
+            float t[CMP_ROWS];
+            int at[CMP_ROWS];
+#pragma unroll
+            for (int u = 0; u < CMP_ROWS; ++u) {
+                const int j = j0 + u * THREADS + threadIdx.x;
+                const int pos = compact_source(a, r, j, j < r.n ? r.keep[j] : -1, false);
+                at[u] = -1;
+                if (pos < 0 || pos >= a.w_stride) continue;
+                const int d = r.start + j, sb = r.src_table[pos >> a.log2_block], db = r.dst_table[d >> a.log2_block];
+                if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) continue;   // its K and V stay, too
+                t[u] = __ldcg(in + pos);
+                at[u] = d;
+            }
+            __syncthreads();      // every thread has read its sources of the chunk
+#pragma unroll
+            for (int u = 0; u < CMP_ROWS; ++u)
+                if (at[u] >= 0) __stcg(out + at[u], t[u]);
+        }
+        return;
+    }
+
+    const int slice = walk >> 1;
+    const bool lead = walk == 0;  // reports what it skips
     const int vecs = 1 << a.log2_vecs;
-    const int col = threadIdx.x & (vecs - 1), r0 = threadIdx.x >> a.log2_vecs;
-    const int rows_per = CMP_THREADS >> a.log2_vecs, chunk = rows_per * CMP_ROWS;
-    const int32_t* keep = a.keep + (static_cast<size_t>(s) * a.keep_heads + (a.keep_heads > 1 ? h : 0)) * a.keep_stride;
-    const int32_t* src_table = a.src_tables + static_cast<size_t>(s) * a.src_blocks;
-    const int32_t* dst_table = a.dst_tables + static_cast<size_t>(s) * a.dst_blocks;
-    uint4* pool = (which ? a.v_cache : a.k_cache) + slice * vecs + col;
-    const long long src_cap = static_cast<long long>(a.src_blocks) << a.log2_block;
-    const long long dst_cap = static_cast<long long>(a.dst_blocks) << a.log2_block;
-    const float* w_in = a.w_in != nullptr ? a.w_in + static_cast<size_t>(row) * a.w_stride : nullptr;
-    float* w_out = a.w_out != nullptr ? a.w_out + static_cast<size_t>(row) * a.w_stride : nullptr;
-    const bool totals = lead && col == 0 && w_out != nullptr;
-    const int nchunks = (n + chunk - 1) / chunk;
+    const int r0 = threadIdx.x >> a.log2_vecs;
+    const int rows_per = THREADS >> a.log2_vecs, chunk = rows_per * CMP_ROWS;
+    uint4* pool = ((walk & 1) ? a.v_cache : a.k_cache) + slice * vecs + (threadIdx.x & (vecs - 1));
+    const int nchunks = (r.n + chunk - 1) / chunk;
 
     // three stages ahead of the store: positions, table entries, rows
-    int pos[CMP_ROWS];
-    int sb[CMP_ROWS], db[CMP_ROWS], sp[CMP_ROWS];
+    int pos[CMP_ROWS], sb[CMP_ROWS], db[CMP_ROWS], off[CMP_ROWS], to[CMP_ROWS];
     uint4 v[CMP_ROWS];
-    float tw[CMP_ROWS];
-    long long to[CMP_ROWS];   // destination vector, or -1
-    int wt[CMP_ROWS];         // destination position of the total, or -1
 
     auto load_pos = [&](int c) {
 #pragma unroll
         for (int u = 0; u < CMP_ROWS; ++u) {
             const int j = c * chunk + u * rows_per + r0;
-            pos[u] = j < n ? keep[j] : -1;
+            pos[u] = j < r.n ? r.keep[j] : -1;
         }
     };
     auto load_entries = [&](int c) {
 #pragma unroll
         for (int u = 0; u < CMP_ROWS; ++u) {
             const int j = c * chunk + u * rows_per + r0;
-            const long long d = static_cast<long long>(start) + j;
-            sp[u] = -1;
-            sb[u] = db[u] = -1;
-            if (j >= n) continue;
-            if (pos[u] < d || pos[u] >= src_cap || d >= dst_cap) {
-                if (lead) flag_error(a.dev_err, PA_DEVERR_COPY);
-                continue;
-            }
-            sp[u] = pos[u];
-            sb[u] = src_table[pos[u] >> a.log2_block];
-            db[u] = dst_table[d >> a.log2_block];
+            const int p = compact_source(a, r, j, pos[u], lead);
+            off[u] = p < 0 ? -1 : p & (a.block_size - 1);
+            if (p < 0) continue;
+            sb[u] = r.src_table[p >> a.log2_block];
+            db[u] = r.dst_table[(r.start + j) >> a.log2_block];
         }
     };
     auto load_rows = [&](int c) {
 #pragma unroll
         for (int u = 0; u < CMP_ROWS; ++u) {
-            const int j = c * chunk + u * rows_per + r0;
             to[u] = -1;
-            wt[u] = -1;
-            if (sp[u] < 0) continue;
+            if (off[u] < 0) continue;
             if (sb[u] < 0 || sb[u] >= a.num_blocks || db[u] < 0 || db[u] >= a.num_blocks) {
                 if (lead) flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
                 continue;
             }
-            const int d = start + j, off = a.block_size - 1;
-            const long long from = ((static_cast<long long>(sb[u]) * a.num_kv_heads + h) * a.block_size + (sp[u] & off)) * a.row_vecs;
-            const long long dest = ((static_cast<long long>(db[u]) * a.num_kv_heads + h) * a.block_size + (d & off)) * a.row_vecs;
-            if (totals && (w_in != w_out || sp[u] != d) && sp[u] < a.w_stride) {
-                tw[u] = __ldcg(w_in + sp[u]);
-                wt[u] = d;
-            }
+            const int d = (r.start + c * chunk + u * rows_per + r0) & (a.block_size - 1);
+            const int from = (sb[u] * a.num_kv_heads + h) * a.block_size + off[u];   // rows of a pool fit 31 bits
+            const int dest = (db[u] * a.num_kv_heads + h) * a.block_size + d;
             if (from == dest) continue;
-            v[u] = __ldcg(pool + from);
+            v[u] = __ldcg(pool + static_cast<size_t>(from) * a.row_vecs);
             to[u] = dest;
         }
     };
@@ -328,15 +435,11 @@ __global__ void __launch_bounds__(CMP_THREADS) compact_kernel(const CompactArgs 
     load_rows(0);
     for (int c = 0; c < nchunks; ++c) {
         uint4 cv[CMP_ROWS];
-        float ct[CMP_ROWS];
-        long long cto[CMP_ROWS];
-        int cwt[CMP_ROWS];
+        int cto[CMP_ROWS];
 #pragma unroll
         for (int u = 0; u < CMP_ROWS; ++u) {
             cv[u] = v[u];
             cto[u] = to[u];
-            ct[u] = tw[u];
-            cwt[u] = wt[u];
         }
         if (c + 1 < nchunks) {
             load_entries(c + 1);
@@ -345,10 +448,8 @@ __global__ void __launch_bounds__(CMP_THREADS) compact_kernel(const CompactArgs 
         }
         __syncthreads();   // every thread has read its sources of chunk c
 #pragma unroll
-        for (int u = 0; u < CMP_ROWS; ++u) {
-            if (cto[u] >= 0) __stcg(pool + cto[u], cv[u]);
-            if (cwt[u] >= 0) __stcg(w_out + cwt[u], ct[u]);
-        }
+        for (int u = 0; u < CMP_ROWS; ++u)
+            if (cto[u] >= 0) __stcg(pool + static_cast<size_t>(cto[u]) * a.row_vecs, cv[u]);
     }
 }
 
@@ -383,11 +484,18 @@ extern "C" int pa_select_tokens(int32_t* keep, int32_t* keep_lens, const float* 
     int cluster = 1;
     while (cluster < SEL_MAX_CLUSTER && weights_stride / cluster > 4096) cluster *= 2;
     const int seg = ((weights_stride + cluster - 1) / cluster + 31) & ~31;
-    a.cached_keys = seg <= SEL_SMEM_KEYS ? seg : 0;
-    const int smem = a.cached_keys * 4;
     static KernelSlot slot;
     if (prepare_kernel(slot, reinterpret_cast<const void*>(select_kernel), SEL_THREADS, SEL_SMEM_KEYS * 4) <= 0)
         return PA_ERR_CUDA;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    // Keys are held where all CTAs are resident with them (227 KB of shared memory
+    // per SM, 17 KB of it counts, at most 4 CTAs) or would not be without them.
+    const int resident = seg <= SEL_SMEM_KEYS ? (227 * 1024) / (seg * 4 + 18 * 1024) : 0;
+    const long long ctas = rows * cluster;
+    const bool hold = resident > 0 && (ctas <= static_cast<long long>(resident < 4 ? resident : 4) * sms || ctas > 4LL * sms);
+    a.cached_keys = hold ? seg : 0;
+    const int smem = a.cached_keys * 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
     cfg.blockDim = dim3(SEL_THREADS);
@@ -416,6 +524,7 @@ extern "C" int pa_compact(void* k_cache, void* v_cache, float* weights_out, cons
     if (keep_heads != 1 && keep_heads != num_kv_heads) return PA_ERR_INVALID_ARG;
     if (!(head_dim == 64 || head_dim == 128)) return PA_ERR_UNSUPPORTED;
     if (!(block_size == 4 || block_size == 8 || block_size == 16 || block_size == 32)) return PA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * num_kv_heads * block_size > INT_MAX) return PA_ERR_UNSUPPORTED;
     if (static_cast<long long>(src_max_blocks) * block_size > INT_MAX ||
         static_cast<long long>(dst_max_blocks) * block_size > INT_MAX)
         return PA_ERR_INVALID_ARG;
@@ -436,8 +545,8 @@ extern "C" int pa_compact(void* k_cache, void* v_cache, float* weights_out, cons
     // that rows are cut into slices of at least 32 bytes (a memory sector).
     int log2_vecs = 0;
     while ((1 << log2_vecs) < row_vecs) ++log2_vecs;
-    const long long walks = 2LL * num_seqs * num_kv_heads;
-    while (log2_vecs > 1 && walks * (row_vecs >> log2_vecs) < 4LL * sms) --log2_vecs;
+    const long long pairs = 2LL * num_seqs * num_kv_heads;
+    while (log2_vecs > 1 && pairs * (row_vecs >> log2_vecs) < 4LL * sms) --log2_vecs;
     CompactArgs a;
     a.k_cache = static_cast<uint4*>(k_cache);
     a.v_cache = static_cast<uint4*>(v_cache);
@@ -461,9 +570,14 @@ extern "C" int pa_compact(void* k_cache, void* v_cache, float* weights_out, cons
     a.row_vecs = row_vecs;
     a.log2_vecs = log2_vecs;
     a.slices = row_vecs >> log2_vecs;
-    const long long ctas = walks * a.slices;
+    a.walks = 2 * a.slices + (weights_out != nullptr ? 1 : 0);
+    const long long ctas = static_cast<long long>(num_seqs) * num_kv_heads * a.walks;
     if (ctas > INT_MAX) return PA_ERR_UNSUPPORTED;
     if (const int rc = device_check(k_cache)) return rc;
-    return launch_status(launch_pdl(compact_kernel, dim3(static_cast<unsigned>(ctas)), dim3(CMP_THREADS), 0,
-                                    as_stream(stream), a));
+    const cudaStream_t st = as_stream(stream);
+    // one CTA per SM or less: longer chunks instead of more CTAs
+    if (ctas <= sms)
+        return launch_status(launch_pdl(compact_kernel<CMP_THREADS_FEW>, dim3(static_cast<unsigned>(ctas)),
+                                        dim3(CMP_THREADS_FEW), 0, st, a));
+    return launch_status(launch_pdl(compact_kernel<CMP_THREADS>, dim3(static_cast<unsigned>(ctas)), dim3(CMP_THREADS), 0, st, a));
 }
