@@ -290,14 +290,19 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
 // loads running ahead of the stores; other CTAs take the other pool, other 16-byte
 // columns of the same rows, and the totals, which never meet.
 //
-// Bound by HBM when there are many walks, by the round trips of a chunk when there
-// are few (positions, table entries and rows are fetched one, two and three stages
-// ahead of the store): then a CTA has 1024 threads, so that a chunk is four times
-// as long.
+// A thread finds the pool rows of one (source, destination) pair of a page of
+// THREADS pairs, its position and table entries fetched one and two pages ahead;
+// the threads that move a row's columns read the pair from shared memory.  Every
+// column's thread finding the rows itself took 1.2 times as long.
+// With many walks that is bound by HBM.  With few (a CTA per SM or less) the round
+// trips of a chunk would bound it: compact_few_kernel's CTAs have 1024 threads,
+// find 8192 pairs at once and keep four chunks of rows in flight.
 // ---------------------------------------------------------------------------
 
-constexpr int CMP_THREADS = 256, CMP_THREADS_FEW = 1024;
-constexpr int CMP_ROWS = 4;   // rows per thread and chunk
+constexpr int CMP_THREADS = 256, CMP_FEW_THREADS = 1024;
+constexpr int CMP_FEW_PAIRS = 8, CMP_FEW_DEPTH = 4;   // pairs per thread and page, chunks in flight
+constexpr int CMP_ROWS = 2;     // rows per thread and chunk
+constexpr int CMP_TOTALS = 4;   // totals per thread and chunk
 
 struct CompactArgs {
     uint4* k_cache;           // [NB][Hkv][B][d] as 16-byte vectors
@@ -338,100 +343,183 @@ __device__ __forceinline__ int compact_source(const CompactArgs& a, const Compac
     return pos;
 }
 
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kernel(const CompactArgs a) {
-    pdl_wait();
-    pdl_launch_dependents();
-    // blockIdx.x = (s * Hkv + h) * walks + walk
-    const int row = blockIdx.x / a.walks, walk = blockIdx.x - row * a.walks;
-    const int s = row / a.num_kv_heads, h = row - s * a.num_kv_heads;
+// blockIdx.x = (s * Hkv + h) * walks + walk: the CTA's (s, h); false if it has nothing to do.
+__device__ __forceinline__ bool compact_begin(const CompactArgs& a, CompactRow& r, int& h, int& walk, int& row) {
+    row = blockIdx.x / a.walks;
+    walk = blockIdx.x - row * a.walks;
+    const int s = row / a.num_kv_heads;
+    h = row - s * a.num_kv_heads;
     const int raw = a.keep_lens[s];
-    CompactRow r;
     r.n = clamp_context(raw, a.keep_stride);
     r.start = a.starts != nullptr ? a.starts[s] : 0;
     if (walk == 0 && threadIdx.x == 0 && h == 0 && (raw != r.n || r.start < 0)) flag_error(a.dev_err, PA_DEVERR_CONTEXT);
-    if (r.start < 0 || r.n == 0) return;
+    if (r.start < 0 || r.n == 0) return false;
     r.keep = a.keep + (static_cast<size_t>(s) * a.keep_heads + (a.keep_heads > 1 ? h : 0)) * a.keep_stride;
     r.src_table = a.src_tables + static_cast<size_t>(s) * a.src_blocks;
     r.dst_table = a.dst_tables + static_cast<size_t>(s) * a.dst_blocks;
+    return true;
+}
 
-    if (walk == 2 * a.slices) {   // the totals: a thread per position
-        const float* in = a.w_in + static_cast<size_t>(row) * a.w_stride;
-        float* out = a.w_out + static_cast<size_t>(row) * a.w_stride;
-        constexpr int CHUNK = THREADS * CMP_ROWS;
-        for (int j0 = 0; j0 < r.n; j0 += CHUNK) {
-            float t[CMP_ROWS];
-            int at[CMP_ROWS];
+// The walk of one (s, h)'s totals: a thread per position.
+__device__ __forceinline__ void compact_totals(const CompactArgs& a, const CompactRow& r, int row) {
+    const float* in = a.w_in + static_cast<size_t>(row) * a.w_stride;
+    float* out = a.w_out + static_cast<size_t>(row) * a.w_stride;
+    const int chunk = blockDim.x * CMP_TOTALS;
+    for (int j0 = 0; j0 < r.n; j0 += chunk) {
+        float t[CMP_TOTALS];
+        int at[CMP_TOTALS];
 #pragma unroll
-            for (int u = 0; u < CMP_ROWS; ++u) {
-                const int j = j0 + u * THREADS + threadIdx.x;
-                const int pos = compact_source(a, r, j, j < r.n ? r.keep[j] : -1, false);
-                at[u] = -1;
-                if (pos < 0 || pos >= a.w_stride) continue;
-                const int d = r.start + j, sb = r.src_table[pos >> a.log2_block], db = r.dst_table[d >> a.log2_block];
-                if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) continue;   // its K and V stay, too
-                t[u] = __ldcg(in + pos);
-                at[u] = d;
-            }
-            __syncthreads();      // every thread has read its sources of the chunk
-#pragma unroll
-            for (int u = 0; u < CMP_ROWS; ++u)
-                if (at[u] >= 0) __stcg(out + at[u], t[u]);
+        for (int u = 0; u < CMP_TOTALS; ++u) {
+            const int j = j0 + u * blockDim.x + threadIdx.x;
+            const int pos = compact_source(a, r, j, j < r.n ? r.keep[j] : -1, false);
+            at[u] = -1;
+            if (pos < 0 || pos >= a.w_stride) continue;
+            const int d = r.start + j, sb = r.src_table[pos >> a.log2_block], db = r.dst_table[d >> a.log2_block];
+            if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) continue;   // its K and V stay, too
+            t[u] = __ldcg(in + pos);
+            at[u] = d;
         }
+        __syncthreads();      // every thread has read its sources of the chunk
+#pragma unroll
+        for (int u = 0; u < CMP_TOTALS; ++u)
+            if (at[u] >= 0) __stcg(out + at[u], t[u]);
+    }
+}
+
+// Pool rows (source, destination) of pair j, from its source position's offset in
+// the block (-1: none) and its table entries; source -1 if nothing moves.  Rows of a
+// pool fit 31 bits.
+__device__ __forceinline__ int2 compact_pair(const CompactArgs& a, const CompactRow& r, int h, int j, int off, int sb,
+                                             int db, bool report) {
+    if (off < 0) return make_int2(-1, 0);
+    if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
+        if (report) flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
+        return make_int2(-1, 0);
+    }
+    const int from = (sb * a.num_kv_heads + h) * a.block_size + off;
+    const int dest = (db * a.num_kv_heads + h) * a.block_size + ((r.start + j) & (a.block_size - 1));
+    return make_int2(from == dest ? -1 : from, dest);
+}
+
+__global__ void __launch_bounds__(CMP_FEW_THREADS, 1) compact_few_kernel(const CompactArgs a) {
+    constexpr int T = CMP_FEW_THREADS, PAGE = T * CMP_FEW_PAIRS, DEPTH = CMP_FEW_DEPTH;
+    extern __shared__ int2 s_page[];   // [PAGE]
+    pdl_wait();
+    pdl_launch_dependents();
+    CompactRow r;
+    int h, walk, row;
+    if (!compact_begin(a, r, h, walk, row)) return;
+    if (walk == 2 * a.slices) {
+        compact_totals(a, r, row);
         return;
     }
-
-    const int slice = walk >> 1;
-    const bool lead = walk == 0;  // reports what it skips
-    const int vecs = 1 << a.log2_vecs;
-    const int r0 = threadIdx.x >> a.log2_vecs;
-    const int rows_per = THREADS >> a.log2_vecs, chunk = rows_per * CMP_ROWS;
-    uint4* pool = ((walk & 1) ? a.v_cache : a.k_cache) + slice * vecs + (threadIdx.x & (vecs - 1));
-    const int nchunks = (r.n + chunk - 1) / chunk;
-
-    // three stages ahead of the store: positions, table entries, rows
-    int pos[CMP_ROWS], sb[CMP_ROWS], db[CMP_ROWS], off[CMP_ROWS], to[CMP_ROWS];
-    uint4 v[CMP_ROWS];
-
-    auto load_pos = [&](int c) {
+    const bool lead = walk == 0;
+    const int vecs = 1 << a.log2_vecs, r0 = threadIdx.x >> a.log2_vecs, rows_per = T >> a.log2_vecs;
+    uint4* pool = ((walk & 1) ? a.v_cache : a.k_cache) + (walk >> 1) * vecs + (threadIdx.x & (vecs - 1));
+    for (int j0 = 0; j0 < r.n; j0 += PAGE) {
+        int off[CMP_FEW_PAIRS], sb[CMP_FEW_PAIRS], db[CMP_FEW_PAIRS];
 #pragma unroll
-        for (int u = 0; u < CMP_ROWS; ++u) {
-            const int j = c * chunk + u * rows_per + r0;
-            pos[u] = j < r.n ? r.keep[j] : -1;
+        for (int u = 0; u < CMP_FEW_PAIRS; ++u) {
+            const int j = j0 + u * T + threadIdx.x;
+            off[u] = j < r.n ? r.keep[j] : -1;
         }
-    };
-    auto load_entries = [&](int c) {
 #pragma unroll
-        for (int u = 0; u < CMP_ROWS; ++u) {
-            const int j = c * chunk + u * rows_per + r0;
-            const int p = compact_source(a, r, j, pos[u], lead);
+        for (int u = 0; u < CMP_FEW_PAIRS; ++u) {
+            const int j = j0 + u * T + threadIdx.x;
+            const int p = compact_source(a, r, j, off[u], lead);
             off[u] = p < 0 ? -1 : p & (a.block_size - 1);
             if (p < 0) continue;
             sb[u] = r.src_table[p >> a.log2_block];
             db[u] = r.dst_table[(r.start + j) >> a.log2_block];
         }
+        __syncthreads();   // the last page's pairs are no longer read
+#pragma unroll
+        for (int u = 0; u < CMP_FEW_PAIRS; ++u)
+            s_page[u * T + threadIdx.x] = compact_pair(a, r, h, j0 + u * T + threadIdx.x, off[u], sb[u], db[u], lead);
+        __syncthreads();
+        // chunk c: the page's pairs [c * rows_per, ...), a thread's row r0 of each
+        const int chunks = (min(PAGE, r.n - j0) + rows_per - 1) / rows_per;
+        uint4 v[DEPTH];
+        int to[DEPTH];
+        auto load = [&](int c, uint4& vv, int& tt) {
+            tt = -1;
+            if (c >= chunks) return;
+            const int2 pair = s_page[c * rows_per + r0];
+            if (pair.x < 0) return;
+            tt = pair.y;
+            vv = __ldcg(pool + static_cast<size_t>(pair.x) * a.row_vecs);
+        };
+#pragma unroll
+        for (int u = 0; u < DEPTH - 1; ++u) load(u, v[u], to[u]);
+        for (int c0 = 0; c0 < chunks; c0 += DEPTH) {
+#pragma unroll
+            for (int u = 0; u < DEPTH; ++u) {
+                load(c0 + u + DEPTH - 1, v[(u + DEPTH - 1) % DEPTH], to[(u + DEPTH - 1) % DEPTH]);
+                __syncthreads();   // every thread has read its source of chunk c0 + u
+                if (to[u] >= 0) __stcg(pool + static_cast<size_t>(to[u]) * a.row_vecs, v[u]);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(CMP_THREADS, 6) compact_kernel(const CompactArgs a) {
+    constexpr int THREADS = CMP_THREADS;
+    pdl_wait();
+    pdl_launch_dependents();
+    CompactRow r;
+    int h, walk, row;
+    if (!compact_begin(a, r, h, walk, row)) return;
+    if (walk == 2 * a.slices) {
+        compact_totals(a, r, row);
+        return;
+    }
+    const int slice = walk >> 1;
+    const bool lead = walk == 0;  // reports what it skips
+    const int vecs = 1 << a.log2_vecs;
+    const int r0 = threadIdx.x >> a.log2_vecs;
+    const int rows_per = THREADS >> a.log2_vecs, chunk = rows_per * CMP_ROWS;
+    const int per_page = vecs / CMP_ROWS;   // chunks of a page of THREADS pairs
+    uint4* pool = ((walk & 1) ? a.v_cache : a.k_cache) + slice * vecs + (threadIdx.x & (vecs - 1));
+    const int nchunks = (r.n + chunk - 1) / chunk;
+    __shared__ int2 s_pair[2][THREADS];     // (source row, destination row) of the pool, source -1: nothing to move
+
+    // the thread's pair of a page: position and table entries under way
+    int pos, off = -1, sb = 0, db = 0;
+    auto load_pos = [&](int page) {
+        const int j = page * THREADS + threadIdx.x;
+        pos = j < r.n ? r.keep[j] : -1;
     };
+    auto load_entries = [&](int page) {
+        const int j = page * THREADS + threadIdx.x;
+        const int p = compact_source(a, r, j, pos, lead);
+        off = p < 0 ? -1 : p & (a.block_size - 1);
+        if (p < 0) return;
+        sb = r.src_table[p >> a.log2_block];
+        db = r.dst_table[(r.start + j) >> a.log2_block];
+    };
+    auto write_pair = [&](int page) {
+        s_pair[page & 1][threadIdx.x] = compact_pair(a, r, h, page * THREADS + threadIdx.x, off, sb, db, lead);
+    };
+
+    uint4 v[CMP_ROWS];
+    int to[CMP_ROWS];
     auto load_rows = [&](int c) {
+        const int2* pairs = s_pair[(c / per_page) & 1] + c % per_page * chunk + r0;
 #pragma unroll
         for (int u = 0; u < CMP_ROWS; ++u) {
-            to[u] = -1;
-            if (off[u] < 0) continue;
-            if (sb[u] < 0 || sb[u] >= a.num_blocks || db[u] < 0 || db[u] >= a.num_blocks) {
-                if (lead) flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
-                continue;
-            }
-            const int d = (r.start + c * chunk + u * rows_per + r0) & (a.block_size - 1);
-            const int from = (sb[u] * a.num_kv_heads + h) * a.block_size + off[u];   // rows of a pool fit 31 bits
-            const int dest = (db[u] * a.num_kv_heads + h) * a.block_size + d;
-            if (from == dest) continue;
-            v[u] = __ldcg(pool + static_cast<size_t>(from) * a.row_vecs);
-            to[u] = dest;
+            const int2 pair = pairs[u * rows_per];
+            to[u] = pair.x < 0 ? -1 : pair.y;
+            if (pair.x >= 0) v[u] = __ldcg(pool + static_cast<size_t>(pair.x) * a.row_vecs);
         }
     };
 
     load_pos(0);
     load_entries(0);
-    if (nchunks > 1) load_pos(1);
+    load_pos(1);
+    write_pair(0);
+    load_entries(1);
+    load_pos(2);
+    __syncthreads();
     load_rows(0);
     for (int c = 0; c < nchunks; ++c) {
         uint4 cv[CMP_ROWS];
@@ -441,11 +529,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kernel(const 
             cv[u] = v[u];
             cto[u] = to[u];
         }
-        if (c + 1 < nchunks) {
-            load_entries(c + 1);
-            if (c + 2 < nchunks) load_pos(c + 2);
-            load_rows(c + 1);
+        if (c % per_page == 0) {   // page p begins: page p + 1's pairs are due
+            const int page = c / per_page;
+            write_pair(page + 1);
+            load_entries(page + 2);
+            load_pos(page + 3);
+            __syncthreads();
         }
+        if (c + 1 < nchunks) load_rows(c + 1);
         __syncthreads();   // every thread has read its sources of chunk c
 #pragma unroll
         for (int u = 0; u < CMP_ROWS; ++u)
@@ -575,9 +666,13 @@ extern "C" int pa_compact(void* k_cache, void* v_cache, float* weights_out, cons
     if (ctas > INT_MAX) return PA_ERR_UNSUPPORTED;
     if (const int rc = device_check(k_cache)) return rc;
     const cudaStream_t st = as_stream(stream);
-    // one CTA per SM or less: longer chunks instead of more CTAs
-    if (ctas <= sms)
-        return launch_status(launch_pdl(compact_kernel<CMP_THREADS_FEW>, dim3(static_cast<unsigned>(ctas)),
-                                        dim3(CMP_THREADS_FEW), 0, st, a));
-    return launch_status(launch_pdl(compact_kernel<CMP_THREADS>, dim3(static_cast<unsigned>(ctas)), dim3(CMP_THREADS), 0, st, a));
+    if (ctas <= sms) {
+        static KernelSlot slot;
+        const int smem = CMP_FEW_THREADS * CMP_FEW_PAIRS * static_cast<int>(sizeof(int2));
+        if (prepare_kernel(slot, reinterpret_cast<const void*>(compact_few_kernel), CMP_FEW_THREADS, smem) <= 0)
+            return PA_ERR_CUDA;
+        return launch_status(launch_pdl(compact_few_kernel, dim3(static_cast<unsigned>(ctas)), dim3(CMP_FEW_THREADS),
+                                        smem, st, a));
+    }
+    return launch_status(launch_pdl(compact_kernel, dim3(static_cast<unsigned>(ctas)), dim3(CMP_THREADS), 0, st, a));
 }
