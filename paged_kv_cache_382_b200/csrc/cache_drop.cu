@@ -31,9 +31,14 @@ namespace pa {
 // every CTA counts its segment's digits in shared memory and adds its counts to
 // the leader's through distributed shared memory (adds return nothing, so nobody
 // waits for them); the leader finds the digit and writes it to every CTA.  Reading
-// all CTAs' counts from every CTA instead took most of a pass.  The segment's keys
-// stay in shared memory over the passes where that leaves the whole launch
-// resident; else they are read again, from L2.
+// all CTAs' counts from every CTA instead took most of a pass.  Keys that share the
+// first digit with the sought one are few, as a rule: they go to the leader, which
+// finds the other digits among them alone (a pass over the cluster costs 6000
+// cycles, half of them barriers).  Only where they are too many for its list, as
+// when most totals are equal, the cluster makes the other passes too.  A segment's
+// keys are read once, all loads at the same time, and stay with their threads, in
+// registers or, 32 to a thread, in shared memory (up to 131072 candidates to a row;
+// longer rows are read again, from L2).
 // ---------------------------------------------------------------------------
 
 constexpr int SEL_THREADS = 512;
@@ -41,7 +46,10 @@ constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_BINS = 2048;
 constexpr int SEL_PER = SEL_BINS / SEL_THREADS;   // bins per thread
 constexpr int SEL_MAX_CLUSTER = 8;
-constexpr int SEL_SMEM_KEYS = 48 * 1024;   // keys a CTA can hold (192 KB)
+constexpr int SEL_LIST = 6144;      // keys the leader's list holds
+// Keys of a CTA that holds them: 4 Q of each thread.
+constexpr int SEL_Q_SHORT = 2, SEL_Q_MIDDLE = 4, SEL_Q_LONG = 8;
+constexpr int sel_keys(int q) { return 4 * q * SEL_THREADS; }
 
 struct SelectArgs {
     int32_t* keep;
@@ -51,7 +59,6 @@ struct SelectArgs {
     const int32_t* budgets;
     int32_t* dev_err;
     int num_kv_heads, weights_stride, keep_stride, recent;
-    int cached_keys;   // segment keys held in shared memory (0: read again from global memory)
 };
 
 // Order-preserving integer of a total: larger totals, larger keys.  NaN counts
@@ -66,34 +73,30 @@ __device__ __forceinline__ uint32_t total_key(float w) {
 // key of no total.
 struct SegmentKeys {
     const float* w;
-    uint32_t* cache;   // null: not held
     int len;
     bool vec;          // w is 16-byte aligned
     __device__ __forceinline__ uint4 load(int i) const {
-        float v[4];
         if (vec && i + 4 <= len) {
             const float4 f = __ldg(reinterpret_cast<const float4*>(w + i));
-            v[0] = f.x;
-            v[1] = f.y;
-            v[2] = f.z;
-            v[3] = f.w;
-            return make_uint4(total_key(v[0]), total_key(v[1]), total_key(v[2]), total_key(v[3]));
+            return make_uint4(total_key(f.x), total_key(f.y), total_key(f.z), total_key(f.w));
         }
         uint32_t k[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) k[j] = i + j < len ? total_key(__ldg(w + i + j)) : 0u;
         return make_uint4(k[0], k[1], k[2], k[3]);
     }
-    __device__ __forceinline__ uint4 get(int i) const {
-        return cache != nullptr ? *reinterpret_cast<const uint4*>(cache + i) : load(i);
-    }
 };
 
-__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a) {
-    extern __shared__ __align__(16) uint32_t s_keys[];
+// Q > 0: the segment's keys are held, Q groups of four per thread (32 registers of
+// them would leave one CTA per SM: those go to shared memory, 16 bytes a thread and
+// group).  Q = 0: read again where they are needed.
+template <int Q>
+__global__ void __launch_bounds__(SEL_THREADS, 2) select_kernel(const SelectArgs a) {
     __shared__ uint32_t hist[2][SEL_BINS];   // by pass parity: one is cleared while the other is in use
     __shared__ int s_scan[33];
-    __shared__ uint32_t s_found[2];          // the pass's digit, and how many keys lie above it
+    __shared__ uint32_t s_found[3];          // the pass's digit, how many keys lie above it, how many have it
+    __shared__ uint32_t s_list[SEL_LIST];    // the leader's: keys with the first digit
+    __shared__ uint32_t s_listed;
     __shared__ int2 s_warp[SEL_WARPS];       // (above, equal) of each warp's sub-segment
     __shared__ int2 s_cta;                   // and of the segment, read by the cluster
     __shared__ int2 s_base;                  // and of the segments before it
@@ -105,6 +108,13 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 #pragma unroll
     for (int i = 0; i < 2 * SEL_PER; ++i) hist[i / SEL_PER][(i % SEL_PER) * SEL_THREADS + tid] = 0;
+    if (tid == 0) s_listed = 0;
+    auto sync_all = [&]() {
+        if (CL > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
     pdl_wait();
     pdl_launch_dependents();
 
@@ -132,46 +142,95 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
     keys.w = a.weights + static_cast<size_t>(row) * a.weights_stride + lo;
     keys.len = len;
     keys.vec = (reinterpret_cast<uintptr_t>(keys.w) & 15u) == 0;
-    keys.cache = nullptr;
-    if (seg <= a.cached_keys) {
-#pragma unroll 4
-        for (int i = 4 * tid; i < len; i += 4 * SEL_THREADS) *reinterpret_cast<uint4*>(s_keys + i) = keys.load(i);
-        keys.cache = s_keys;
+    // warp w takes a contiguous part of the segment, a lane four keys at a time
+    const int part = Q > 0 ? 128 * Q : ((len + SEL_WARPS - 1) / SEL_WARPS + 127) & ~127;
+    const int w0 = min(len, warp * part), w1 = min(len, w0 + part);
+    extern __shared__ __align__(16) uint4 s_held[];   // [Q][SEL_THREADS] for Q = SEL_Q_LONG
+    constexpr bool IN_SHARED = Q == SEL_Q_LONG;
+    uint4 held[Q > 0 && !IN_SHARED ? Q : 1];
+    if constexpr (Q > 0) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const uint4 k4 = keys.load(w0 + 128 * q + 4 * lane);
+            if constexpr (IN_SHARED)
+                s_held[q * SEL_THREADS + tid] = k4;
+            else
+                held[q] = k4;
+        }
     }
-    cluster.sync();            // cleared counts (the leader's before anybody adds), own keys
+    // f(four keys, index of the first) for the lane's keys, in order
+    auto each = [&](auto&& f) {
+        if constexpr (IN_SHARED) {
+#pragma unroll 2
+            for (int q = 0; q < Q; ++q) f(s_held[q * SEL_THREADS + tid], w0 + 128 * q + 4 * lane);
+        } else if constexpr (Q > 0) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) f(held[q], w0 + 128 * q + 4 * lane);
+        } else {
+#pragma unroll 2
+            for (int i0 = w0; i0 < w1; i0 += 128) f(keys.load(i0 + 4 * lane), i0 + 4 * lane);
+        }
+    };
+    sync_all();                // cleared counts (the leader's before anybody adds)
 
     uint32_t prefix = 0;       // digits found so far
     uint32_t want = k;         // rank of the sought key among those with the prefix
     int shift = 32;
+    // counts the digits (of `bits` bits, above `shift`) of four keys that have the prefix
+    auto count4 = [&](uint32_t* h, const uint4& k4, int i, int end, int pass, int hi_shift, uint32_t mask) {
+        const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+        // neighbours with one digit (zeros above all) add once
+        uint32_t at = 0, count = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = i + j < end && (pass == 0 || (kk[j] >> hi_shift) == prefix);
+            if (!in) continue;
+            const uint32_t d = (kk[j] >> shift) & mask;
+            if (count != 0 && d != at) {
+                atomicAdd(&h[at], count);
+                count = 0;
+            }
+            at = d;
+            ++count;
+        }
+        if (count != 0) atomicAdd(&h[at], count);
+    };
+    // the digit that holds the wanted rank, told to CTAs 0 .. tell - 1; whole CTA, counts complete
+    auto find = [&](const uint32_t* h, int tell) {
+        // thread t owns SEL_PER bins counted from the top
+        uint32_t cnt[SEL_PER], sum = 0;
+#pragma unroll
+        for (int j = 0; j < SEL_PER; ++j) {
+            cnt[j] = h[SEL_BINS - 1 - (tid * SEL_PER + j)];
+            sum += cnt[j];
+        }
+        int total;
+        uint32_t before = static_cast<uint32_t>(cta_exclusive_scan(static_cast<int>(sum), &total, s_scan));
+#pragma unroll
+        for (int j = 0; j < SEL_PER; ++j) {
+            if (before < want && want <= before + cnt[j]) {   // exactly one thread and bin
+                for (int c = 0; c < tell; ++c) {
+                    uint32_t* to = cluster.map_shared_rank(s_found, c);
+                    to[0] = SEL_BINS - 1 - (tid * SEL_PER + j);
+                    to[1] = before;
+                    to[2] = cnt[j];
+                }
+            }
+            before += cnt[j];
+        }
+        __syncthreads();
+    };
+    bool done = false;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
+    for (int pass = 0; pass < 3 && !done; ++pass) {
         const int bits = pass < 2 ? 11 : 10;
         const int hi_shift = shift;
         shift -= bits;
         const uint32_t mask = (1u << bits) - 1u;
         uint32_t* h = hist[pass & 1];
-#pragma unroll 2
-        for (int i = 4 * tid; i < len; i += 4 * SEL_THREADS) {
-            const uint4 k4 = keys.get(i);
-            const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
-            // neighbours with one digit (zeros above all) add once
-            uint32_t at = 0, count = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = i + j < len && (pass == 0 || (kk[j] >> hi_shift) == prefix);
-                if (!in) continue;
-                const uint32_t d = (kk[j] >> shift) & mask;
-                if (count != 0 && d != at) {
-                    atomicAdd(&h[at], count);
-                    count = 0;
-                }
-                at = d;
-                ++count;
-            }
-            if (count != 0) atomicAdd(&h[at], count);
-        }
+        each([&](const uint4& k4, int i) { count4(h, k4, i, w1, pass, hi_shift, mask); });
+        __syncthreads();
         if (CL > 1) {
-            __syncthreads();
             if (rank != 0) {
                 uint32_t* lead = cluster.map_shared_rank(h, 0);
 #pragma unroll
@@ -180,42 +239,62 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
                     if (c != 0) atomicAdd(lead + j * SEL_THREADS + tid, c);
                 }
             }
+            cluster.sync();    // the leader has every segment's counts
         }
-        cluster.sync();        // the leader has every segment's counts
-        if (rank == 0) {
-            // thread t owns SEL_PER bins counted from the top
-            uint32_t cnt[SEL_PER], sum = 0;
-#pragma unroll
-            for (int j = 0; j < SEL_PER; ++j) {
-                cnt[j] = h[SEL_BINS - 1 - (tid * SEL_PER + j)];
-                sum += cnt[j];
-            }
-            int total;
-            uint32_t before = static_cast<uint32_t>(cta_exclusive_scan(static_cast<int>(sum), &total, s_scan));
-#pragma unroll
-            for (int j = 0; j < SEL_PER; ++j) {
-                if (before < want && want <= before + cnt[j]) {   // exactly one thread and bin
-                    for (int c = 0; c < CL; ++c) {
-                        uint32_t* to = cluster.map_shared_rank(s_found, c);
-                        to[0] = SEL_BINS - 1 - (tid * SEL_PER + j);
-                        to[1] = before;
-                    }
-                }
-                before += cnt[j];
-            }
-            __syncthreads();   // counts read by all before they are cleared
-        }
+        if (rank == 0) find(h, CL);
 #pragma unroll
         for (int j = 0; j < SEL_PER; ++j) h[j * SEL_THREADS + tid] = 0;   // for the pass after the next
-        cluster.sync();        // the digit is known
+        sync_all();            // the digit is known
         prefix = (prefix << bits) | s_found[0];
         want -= s_found[1];
+        if (pass > 0 || s_found[2] > SEL_LIST) continue;
+
+        // few enough: the leader takes the keys with this digit and goes on alone
+        done = true;
+        int mine = 0;
+        each([&](const uint4& k4, int i) {
+            const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mine += i + j < w1 && (kk[j] >> shift) == prefix;
+        });
+        const int upto = warp_inclusive_scan(mine);
+        uint32_t at = 0;
+        if (lane == 31 && upto > 0) at = atomicAdd(cluster.map_shared_rank(&s_listed, 0), static_cast<uint32_t>(upto));
+        at = __shfl_sync(FULL_MASK, at, 31) + upto - mine;
+        uint32_t* list = cluster.map_shared_rank(s_list, 0);
+        each([&](const uint4& k4, int i) {
+            const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j < w1 && (kk[j] >> shift) == prefix) list[at++] = kk[j];
+        });
+        sync_all();            // the list is complete
+        if (rank == 0) {
+            const int n_list = static_cast<int>(s_listed);
+#pragma unroll 1
+            for (int p = 1; p < 3; ++p) {
+                const int b = p < 2 ? 11 : 10, hi = shift;
+                shift -= b;
+                for (int i = tid; i < n_list; i += SEL_THREADS)
+                    if ((s_list[i] >> hi) == prefix) atomicAdd(&hist[p & 1][(s_list[i] >> shift) & ((1u << b) - 1u)], 1u);
+                __syncthreads();
+                find(hist[p & 1], 1);
+                prefix = (prefix << b) | s_found[0];
+                want -= s_found[1];
+                __syncthreads();   // s_found is written again
+            }
+            if (tid < CL) {
+                uint32_t* to = cluster.map_shared_rank(s_found, tid);
+                to[0] = prefix;
+                to[1] = want;
+            }
+        }
+        sync_all();
+        prefix = s_found[0];
+        want = s_found[1];
     }
     // want = how many of the keys equal to prefix stay, the first ones by position
 
-    // warp w takes a contiguous part of the segment, a lane four keys at a time
-    const int part = ((len + SEL_WARPS - 1) / SEL_WARPS + 127) & ~127;
-    const int w0 = min(len, warp * part), w1 = min(len, w0 + part);
     auto tell = [&](const uint4& k4, int i, int (&up)[4], int (&eq)[4]) {
         const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
@@ -225,13 +304,12 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
         }
     };
     int above = 0, equal = 0;
-#pragma unroll 2
-    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    each([&](const uint4& k4, int i) {
         int up[4], eq[4];
-        tell(keys.get(i), i, up, eq);
+        tell(k4, i, up, eq);
         above += up[0] + up[1] + up[2] + up[3];
         equal += eq[0] + eq[1] + eq[2] + eq[3];
-    }
+    });
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         above += __shfl_xor_sync(FULL_MASK, above, off);
@@ -245,7 +323,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
         if (lane < SEL_WARPS) s_warp[lane] = make_int2(ix - x.x, iy - x.y);
         if (lane == 31) s_cta = make_int2(ix, iy);
     }
-    cluster.sync();
+    sync_all();
     if (warp == 0) {
         int2 x = make_int2(0, 0);
         if (lane < rank) x = *cluster.map_shared_rank(&s_cta, lane);
@@ -256,13 +334,12 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
         }
         if (lane == 0) s_base = x;
     }
-    cluster.sync();   // and s_cta is no longer read by the cluster
+    sync_all();       // and s_cta is no longer read by the cluster
     int base_above = s_warp[warp].x + s_base.x, base_equal = s_warp[warp].y + s_base.y;
     const int quota = static_cast<int>(want);
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-        const int i = i0 + 4 * lane;
-        int up[4] = {0, 0, 0, 0}, eq[4] = {0, 0, 0, 0};
-        if (i < w1) tell(keys.get(i), i, up, eq);
+    each([&](const uint4& k4, int i) {
+        int up[4], eq[4];
+        tell(k4, i, up, eq);
         const int nu = up[0] + up[1] + up[2] + up[3], ne = eq[0] + eq[1] + eq[2] + eq[3];
         // both counts of a lane in one scan: at most 128 each
         const int inc = warp_inclusive_scan(nu | (ne << 16));
@@ -276,7 +353,7 @@ __global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a)
         const int all = __shfl_sync(FULL_MASK, inc, 31);
         base_above += all & 0xffff;
         base_equal += all >> 16;
-    }
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -572,25 +649,28 @@ extern "C" int pa_select_tokens(int32_t* keep, int32_t* keep_lens, const float* 
     a.weights_stride = weights_stride;
     a.keep_stride = keep_stride;
     a.recent = recent;
-    int cluster = 1;
-    while (cluster < SEL_MAX_CLUSTER && weights_stride / cluster > 4096) cluster *= 2;
-    const int seg = ((weights_stride + cluster - 1) / cluster + 31) & ~31;
-    static KernelSlot slot;
-    if (prepare_kernel(slot, reinterpret_cast<const void*>(select_kernel), SEL_THREADS, SEL_SMEM_KEYS * 4) <= 0)
-        return PA_ERR_CUDA;
     const int sms = current_sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
-    // Keys are held where all CTAs are resident with them (227 KB of shared memory
-    // per SM, 17 KB of it counts, at most 4 CTAs) or would not be without them.
-    const int resident = seg <= SEL_SMEM_KEYS ? (227 * 1024) / (seg * 4 + 18 * 1024) : 0;
-    const long long ctas = rows * cluster;
-    const bool hold = resident > 0 && (ctas <= static_cast<long long>(resident < 4 ? resident : 4) * sms || ctas > 4LL * sms);
-    a.cached_keys = hold ? seg : 0;
-    const int smem = a.cached_keys * 4;
+    // As few CTAs to a row as hold its keys in registers, then more while that leaves
+    // SMs idle: a cluster's barriers cost more than longer segments do.
+    int cluster = 1;
+    auto segment = [&](int c) { return ((weights_stride + c - 1) / c + 31) & ~31; };
+    while (cluster < SEL_MAX_CLUSTER && segment(cluster) > sel_keys(SEL_Q_LONG)) cluster *= 2;
+    while (cluster < SEL_MAX_CLUSTER && rows * cluster < sms && segment(cluster) > sel_keys(SEL_Q_SHORT)) cluster *= 2;
+    const int seg = segment(cluster);
+    auto kern = seg <= sel_keys(SEL_Q_SHORT)    ? select_kernel<SEL_Q_SHORT>
+                : seg <= sel_keys(SEL_Q_MIDDLE) ? select_kernel<SEL_Q_MIDDLE>
+                : seg <= sel_keys(SEL_Q_LONG)   ? select_kernel<SEL_Q_LONG>
+                                                : select_kernel<0>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
     cfg.blockDim = dim3(SEL_THREADS);
-    cfg.dynamicSmemBytes = smem;
+    if (seg > sel_keys(SEL_Q_MIDDLE) && seg <= sel_keys(SEL_Q_LONG)) {
+        static KernelSlot slot;
+        cfg.dynamicSmemBytes = sel_keys(SEL_Q_LONG) * 4;
+        if (prepare_kernel(slot, reinterpret_cast<const void*>(kern), SEL_THREADS, sel_keys(SEL_Q_LONG) * 4) <= 0)
+            return PA_ERR_CUDA;
+    }
     cfg.stream = as_stream(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -601,7 +681,7 @@ extern "C" int pa_select_tokens(int32_t* keep, int32_t* keep_lens, const float* 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return launch_status(cudaLaunchKernelEx(&cfg, select_kernel, a));
+    return launch_status(cudaLaunchKernelEx(&cfg, kern, a));
 }
 
 extern "C" int pa_compact(void* k_cache, void* v_cache, float* weights_out, const float* weights_in, int weights_stride,

@@ -224,15 +224,15 @@ def test_select_matches_oracle(pa, kind, recent):
 
 
 @pytest.mark.parametrize("stride,kind", [(4097, "weights"), (9001, "ties"), (20000, "weights"), (40001, "zeros"),
-                                         (70000, "weights")])
+                                         (70000, "weights"), (131072, "ties"), (131073, "weights")])
 def test_select_long_rows_over_clusters(pa, stride, kind):
     lens = [stride, stride - 1, 1, stride // 3, 0]
     budgets = [stride // 4, 1, 7, stride // 3 - 1, 3]
     check_select(pa, totals((5, 2, stride), 6, kind), lens, budgets, 129, stride // 3)
 
 
-def test_select_rows_longer_than_shared_memory(pa):
-    """Segments past 48 K keys per CTA of the cluster are read again instead of held."""
+def test_select_rows_too_long_to_hold(pa):
+    """Rows of more than 8 x 16384 candidates are read again in every pass instead of held."""
     stride = 8 * 48 * 1024 + 1000
     w = totals((1, 1, stride), 7, "weights")
     k = 5000
