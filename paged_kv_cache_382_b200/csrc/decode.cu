@@ -1065,7 +1065,7 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 // 2b. attend, fp32: CUDA cores, one warp per token, lanes split the head dim
 // ---------------------------------------------------------------------------
 
-template <int D, bool LOGITS>
+template <int D>
 __global__ void __launch_bounds__(128, 2) attend_f32_kernel(const DecodeArgs a) {
     constexpr int W = 4, J = D / 32;
     __shared__ float mm[W * 8], ml[W * 8];
@@ -1109,7 +1109,6 @@ __global__ void __launch_bounds__(128, 2) attend_f32_kernel(const DecodeArgs a) 
             const int phys = table_row(a, s)[t / B];
             if (phys < 0 || phys >= a.num_blocks) {
                 if (lane == 0) flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
-                if (LOGITS && lane < gsub) logits_row(a, s, kvh, hg, t)[lane] = NEG_INF;   // takes no part
                 continue;
             }
             const size_t rowi = ((static_cast<size_t>(phys) * a.num_kv_heads + kvh) * B + t % B) * D;
@@ -1128,7 +1127,6 @@ __global__ void __launch_bounds__(128, 2) attend_f32_kernel(const DecodeArgs a) 
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(FULL_MASK, dot, off);
                 const float x = dot * a.scale_log2;
-                if (LOGITS && lane == 0) logits_row(a, s, kvh, hg, t)[n] = x;
                 const float mn = fmaxf(m[n], x);
                 const float al = exp2_approx(m[n] - mn);
                 const float pw = exp2_approx(x - mn);
@@ -1152,7 +1150,150 @@ __global__ void __launch_bounds__(128, 2) attend_f32_kernel(const DecodeArgs a) 
 #pragma unroll
             for (int j = 0; j < J; ++j) mo[(warp * 8 + n) * D + lane + 32 * j] = acc[n][j];
         __syncthreads();
-        combine_store<W, D, LOGITS>(a, mm, ml, mo, s_rows, p, gsub);
+        combine_store<W, D, false>(a, mm, ml, mo, s_rows, p, gsub);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 2c. attend, fp32, keeping the logits (pa_decode_weights)
+//
+// A warp takes 32 tokens at a time.  For q.K a lane owns a token and reads its row
+// (the row's sectors come through L1), so a dot product needs no exchange: the warp
+// reduces one maximum per head and 32 tokens.  For p.V a lane owns four columns,
+// rows are read whole, and each weight comes from its token's lane.  About 50
+// instructions per token at 5 heads; a token per warp with its dot products summed
+// over the lanes (2b) is bound by those exchanges and by one round trip per token:
+// 10 sequences of 23746 to 48212 tokens, 20 / 4 heads, d 128: 1250 us that way.
+// ---------------------------------------------------------------------------
+
+template <int D>
+__global__ void __launch_bounds__(128, 4) attend_f32_logits_kernel(const DecodeArgs a) {
+    constexpr int W = 4, VL = D / 4, TPI = 32 / VL;   // lanes per value row, rows read together
+    __shared__ float mm[W * 8], ml[W * 8];
+    __shared__ __align__(16) float mo[W * 8 * D];
+    __shared__ float4 s_q[8][VL];
+    __shared__ int3 s_rows[8];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int per_item = a.num_kv_heads * a.head_groups;
+    const long long units = static_cast<long long>(*a.ws_count) * per_item;
+    const int P = a.partition_size, B = a.block_size;
+    const float4* kc = static_cast<const float4*>(a.k_cache);
+    const float4* vc = static_cast<const float4*>(a.v_cache);
+    const float4* qp = static_cast<const float4*>(a.q);
+    const float sl2 = a.scale_log2;
+
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int4 item = a.ws_items[u / per_item];
+        const int r = static_cast<int>(u % per_item);
+        const int kvh = r / a.head_groups, hg = r - (r / a.head_groups) * a.head_groups;
+        int s, p, count, stream;
+        split_item(item.x, a.max_parts, s, p, count, stream);   // this path is planned unpacked: count == 1
+        const int ctx = item.y;
+        const int t0 = p * P, t1 = min(t0 + P, ctx);
+        const int nparts = (ctx + P - 1) / P;
+        const int gsub = min(8, a.group - hg * 8);
+        const int head0 = kvh * a.group + hg * 8;
+        const int32_t* trow = table_row(a, s);
+        for (int i = tid; i < gsub * VL; i += W * 32)
+            s_q[i / VL][i % VL] = qp[(static_cast<size_t>(s) * a.num_heads + head0 + i / VL) * VL + i % VL];
+        __syncthreads();   // and the previous unit's epilogue is done with the merge buffers
+
+        float m[8], l[8];
+        float4 acc[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            m[n] = NEG_INF;
+            l[n] = 0.f;
+            acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int tb = t0 + 32 * warp; tb < t1; tb += 32 * W) {
+            const int t = tb + lane;
+            const int phys = t < t1 ? trow[t >> a.log2_block] : -1;
+            int row = -1;   // rows of a pool fit 31 bits
+            if (phys >= 0 && phys < a.num_blocks)
+                row = (phys * a.num_kv_heads + kvh) * B + (t & (B - 1));
+            else if (t < t1)
+                flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
+            float x[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[n] = 0.f;
+            if (row >= 0) {
+                const float4* k = kc + static_cast<size_t>(row) * VL;
+#pragma unroll 8
+                for (int i = 0; i < VL; ++i) {
+                    const float4 kv = __ldg(k + i);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        if (n < gsub) {
+                            const float4 q = s_q[n][i];
+                            x[n] = fmaf(q.x, kv.x, x[n]);
+                            x[n] = fmaf(q.y, kv.y, x[n]);
+                            x[n] = fmaf(q.z, kv.z, x[n]);
+                            x[n] = fmaf(q.w, kv.w, x[n]);
+                        }
+                    }
+                }
+            }
+            float* out_x = logits_row(a, s, kvh, hg, t);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                if (n < gsub) {
+                    x[n] = row >= 0 ? x[n] * sl2 : NEG_INF;   // a bad block's tokens take no part
+                    if (t < t1) out_x[n] = x[n];
+                    float mx = x[n];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, off));
+                    const float mn = fmaxf(m[n], mx), base = mn == NEG_INF ? 0.f : mn;
+                    const float al = exp2_approx(m[n] - base);
+                    m[n] = mn;
+                    x[n] = exp2_approx(x[n] - base);
+                    l[n] = fmaf(l[n], al, x[n]);
+                    acc[n].x *= al;
+                    acc[n].y *= al;
+                    acc[n].z *= al;
+                    acc[n].w *= al;
+                }
+            }
+            const int here = min(32, t1 - tb);
+#pragma unroll 4
+            for (int i = 0; i < here; i += TPI) {
+                const int tok = i + lane / VL;
+                const int vrow = __shfl_sync(FULL_MASK, row, tok);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (vrow >= 0) v = __ldg(vc + static_cast<size_t>(vrow) * VL + lane % VL);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    if (n < gsub) {
+                        const float w = __shfl_sync(FULL_MASK, x[n], tok);
+                        acc[n].x = fmaf(w, v.x, acc[n].x);
+                        acc[n].y = fmaf(w, v.y, acc[n].y);
+                        acc[n].z = fmaf(w, v.z, acc[n].z);
+                        acc[n].w = fmaf(w, v.w, acc[n].w);
+                    }
+                }
+            }
+        }
+        if (tid < 8) s_rows[tid] = make_int3(s, head0 + tid, nparts);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) l[n] += __shfl_xor_sync(FULL_MASK, l[n], off);
+            if (VL == 16) {   // the two half warps hold the same columns of different tokens
+                acc[n].x += __shfl_xor_sync(FULL_MASK, acc[n].x, 16);
+                acc[n].y += __shfl_xor_sync(FULL_MASK, acc[n].y, 16);
+                acc[n].z += __shfl_xor_sync(FULL_MASK, acc[n].z, 16);
+                acc[n].w += __shfl_xor_sync(FULL_MASK, acc[n].w, 16);
+            }
+            if (lane == 0) {
+                mm[warp * 8 + n] = m[n];
+                ml[warp * 8 + n] = l[n];
+            }
+            if (lane < VL) *reinterpret_cast<float4*>(mo + (warp * 8 + n) * D + 4 * lane) = acc[n];
+        }
+        __syncthreads();
+        combine_store<W, D, true>(a, mm, ml, mo, s_rows, p, gsub);
     }
 }
 
@@ -1502,7 +1643,7 @@ int launch_attend_bf16(const DecodeArgs& a, cudaStream_t st, long long unit_boun
 template <int D, bool LOGITS>
 int launch_attend_f32(const DecodeArgs& a, cudaStream_t st, long long unit_bound) {
     static KernelSlot slot;
-    auto kern = attend_f32_kernel<D, LOGITS>;
+    auto kern = LOGITS ? attend_f32_logits_kernel<D> : attend_f32_kernel<D>;
     const int per_sm = prepare_kernel(slot, reinterpret_cast<const void*>(kern), 128, 0);
     const int sms = current_sm_count();
     if (per_sm <= 0 || sms <= 0) return PA_ERR_CUDA;
