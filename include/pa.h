@@ -333,10 +333,10 @@ PA_API int pa_decode_noalloc(void* out, pa_dtype out_dtype, const void* q, const
  * Arithmetic: as for pa_decode.  The work is cut over the GPU by the whole batch, so the same
  * call gives the same bits every time, but a sequence's rounding may differ in another batch.
  * On bf16 pools with block_size 8, 16 or 32 (pa_tree_uses_tensor_cores) the products run as
- * tcgen05 MMAs over tiles of 128 query rows; elsewhere on the CUDA cores in fp32.  On the
- * tensor cores every K/V value in the context must be finite: a non-finite value reaches
- * every row of its sequence and kv head (0 * NaN), whether the row sees that token or not.
- * Launches two kernels (attention, join) on `stream`.
+ * tcgen05 MMAs over tiles of 128 query rows; elsewhere on the CUDA cores in fp32.  A
+ * non-finite K or V of a node reaches the rows that see it and no others.
+ * Launches two kernels (attention, join) on `stream`.  Calls that may overlap in time need
+ * workspaces of their own.
  */
 #define PA_TREE_MAX_WORDS 8   /* 512 nodes per sequence */
 PA_API size_t pa_tree_workspace_bytes(int num_tokens, int num_heads, int head_dim);
@@ -382,6 +382,7 @@ PA_API int pa_tree_mask(const int32_t* parents, int num_nodes, int mask_words, i
  * is a variant that serves every sequence by itself (shared blocks are read once
  * per sequence).  At most 256 query heads per kv head.  Totals are sums in fp32,
  * heads in order.  A token in a block whose id is flagged receives weight zero.
+ * Calls that may overlap in time need workspaces of their own.
  */
 PA_API size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int head_dim,
                                                 int max_context_len, int partition_size);

@@ -317,7 +317,8 @@ void rekey(pa_block_manager* m, Sequence& sq, int64_t unchanged, int64_t num_tok
 }  // namespace
 
 extern "C" int pa_bm_compact(pa_block_manager* m, int num_seqs, const int64_t* seq_ids, const int64_t* unchanged,
-                             const int64_t* num_tokens, const int32_t* token_ids, int64_t* copies, int* num_copies) {
+                             const int64_t* num_tokens, const int32_t* token_ids, int64_t* copies,
+                             int* num_copies) try {
     if (!m || num_seqs < 0 || !num_copies) return PA_ERR_INVALID_ARG;
     if (num_seqs > 0 && (!seq_ids || !unchanged || !num_tokens || !copies)) return PA_ERR_INVALID_ARG;
     const int64_t B = m->block_size;
@@ -378,6 +379,8 @@ extern "C" int pa_bm_compact(pa_block_manager* m, int num_seqs, const int64_t* s
         if (ids != nullptr) ids += num_tokens[k] - unchanged[k];
     }
     return PA_OK;
+} catch (const std::bad_alloc&) {
+    return PA_ERR_WORKSPACE;   // no host memory: no exception leaves a C entry point
 }
 
 extern "C" int pa_bm_block_table(const pa_block_manager* m, int64_t seq_id, int32_t* out, int max_blocks,

@@ -57,8 +57,9 @@ struct TreeArgs {
     int out_f32;
 };
 
-// CTAs a launch may have (and partial pairs the workspace holds).
-constexpr int TREE_CTAS_MAX = 160;
+// CTAs a launch may have (and partial pairs the workspace holds): one per SM on the
+// tensor cores, two on the CUDA cores.
+constexpr int TREE_TC_CTAS = 160, TREE_SIMT_CTAS = 2 * TREE_TC_CTAS, TREE_CTAS_MAX = TREE_SIMT_CTAS;
 // Sequences are found in windows of 32; the windows' sums sit in shared memory.
 constexpr int TREE_WINDOWS_MAX = 4096;
 // What a unit costs besides its tiles (the host bounds W by INT_MAX).

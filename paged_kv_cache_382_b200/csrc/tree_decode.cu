@@ -24,7 +24,8 @@ namespace {
 // thread (ty, tx) holds rows 4 ty .. 4 ty + 3 of S for tokens 4 tx .. and of O
 // for D / 16 columns, so each operand read from shared memory feeds four FMAs.
 // Q and K are stored transposed ([d][row]) for that; softmax statistics of a row
-// live in the 16 threads that share it.
+// live in the 16 threads that share it.  The weights take K's place once S is
+// complete, so that two CTAs fit an SM and one loads while the other computes.
 // ---------------------------------------------------------------------------
 
 constexpr int TS_ROWS = 64;
@@ -34,7 +35,7 @@ constexpr int TS_PAD = 68;   // floats per transposed row: 16-byte aligned, colu
 
 template <int D>
 constexpr int tree_simt_smem() {
-    return (2 * D * TS_PAD + TS_KT * D + TS_ROWS * TS_PAD) * 4;
+    return (2 * D * TS_PAD + TS_KT * D) * 4;
 }
 
 template <typename T>
@@ -50,13 +51,13 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(TS_THREADS) tree_simt_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs a) {
     constexpr int OC = D / 16;   // output columns per thread
     extern __shared__ __align__(16) uint8_t smem_dyn[];
     float* sQ = reinterpret_cast<float*>(smem_dyn);   // [D][TS_PAD]
     float* sK = sQ + D * TS_PAD;                      // [D][TS_PAD]
     float* sV = sK + D * TS_PAD;                      // [TS_KT][D]
-    float* sP = sV + TS_KT * D;                       // [TS_ROWS][TS_PAD]
+    float* sP = sK;                                   // [TS_ROWS][TS_PAD], once S is complete
     __shared__ int s_row[TS_KT];                      // pool row of each token of the tile, or -1
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const T* q = static_cast<const T*>(a.q);
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(TS_THREADS) tree_simt_kernel(const TreeArgs a)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[i][j] = fmaf(qa[i], ka[j], x[i][j]);
             }
+            __syncthreads();   // K is no longer read: P goes there
             uint32_t in = 0;   // tokens of this thread that take part
 #pragma unroll
             for (int j = 0; j < 4; ++j) in |= (s_row[4 * tx + j] >= 0 ? 1u : 0u) << j;
@@ -367,19 +369,21 @@ inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct TreeWs {
     size_t line, recs, ml, acc, total;
-    int rows;
+    int tc_rows, simt_rows;   // rows of a partial
 };
 
 inline TreeWs tree_ws(long long num_tokens, int num_heads, int head_dim) {
     TreeWs w;
-    const int most = tree_tc_rows() > TS_ROWS ? tree_tc_rows() : TS_ROWS;
     const long long rows = num_tokens * num_heads;   // no unit has more
-    w.rows = static_cast<int>(rows < most ? rows : most);
+    w.tc_rows = static_cast<int>(rows < tree_tc_rows() ? rows : tree_tc_rows());
+    w.simt_rows = static_cast<int>(rows < TS_ROWS ? rows : TS_ROWS);
+    const size_t tc = 2ull * TREE_TC_CTAS * w.tc_rows, simt = 2ull * TREE_SIMT_CTAS * w.simt_rows;
+    const size_t most = tc > simt ? tc : simt;
     w.line = 0;
     w.recs = 256;
     w.ml = w.recs + up256(TREE_CTAS_MAX * sizeof(TreeRecord));
-    w.acc = w.ml + up256(2 * TREE_CTAS_MAX * static_cast<size_t>(w.rows) * sizeof(float2));
-    w.total = w.acc + up256(2 * TREE_CTAS_MAX * static_cast<size_t>(w.rows) * head_dim * sizeof(float));
+    w.acc = w.ml + up256(most * sizeof(float2));
+    w.total = w.acc + up256(most * head_dim * sizeof(float));
     return w;
 }
 
@@ -447,7 +451,8 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
     a.recs = reinterpret_cast<TreeRecord*>(ws + L.recs);
     a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
     a.part_acc = reinterpret_cast<float*>(ws + L.acc);
-    a.part_rows = L.rows;
+    const bool tc = tree_tc_eligible(dtype, block_size);
+    a.part_rows = tc ? L.tc_rows : L.simt_rows;
     a.mask_words32 = 2 * mask_words;
     a.num_seqs = num_seqs;
     a.num_tokens = num_tokens;
@@ -465,9 +470,9 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
     if (const int rc = device_check(k_cache)) return rc;
     const int sms = current_sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
-    const int ctas = sms < TREE_CTAS_MAX ? sms : TREE_CTAS_MAX;
+    const int ctas = tc ? (sms < TREE_TC_CTAS ? sms : TREE_TC_CTAS) : (2 * sms < TREE_SIMT_CTAS ? 2 * sms : TREE_SIMT_CTAS);
     int rc;
-    if (tree_tc_eligible(dtype, block_size))
+    if (tc)
         rc = launch_tree_tc(a, head_dim, ctas, st);
     else if (dtype == PA_F32)
         rc = head_dim == 128 ? launch_tree_simt<128, float>(a, ctas, st) : launch_tree_simt<64, float>(a, ctas, st);
@@ -475,7 +480,7 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
         rc = head_dim == 128 ? launch_tree_simt<128, __nv_bfloat16>(a, ctas, st)
                              : launch_tree_simt<64, __nv_bfloat16>(a, ctas, st);
     if (rc != PA_OK || ctas < 2) return rc;
-    const dim3 grid(ctas - 1, (L.rows + TJ_ROWS - 1) / TJ_ROWS);
+    const dim3 grid(ctas - 1, (a.part_rows + TJ_ROWS - 1) / TJ_ROWS);
     return launch_status(head_dim == 128 ? launch_pdl(tree_join_kernel<128>, grid, dim3(TJ_THREADS), 0, st, a, ctas)
                                          : launch_pdl(tree_join_kernel<64>, grid, dim3(TJ_THREADS), 0, st, a, ctas));
 }

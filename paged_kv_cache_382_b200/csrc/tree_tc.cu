@@ -94,6 +94,7 @@ struct TreeShared {
     uint64_t p_full[2][2];         // its weights are (128 arrivals)
     uint64_t o_done[2][2];         // its P.V has finished
     uint64_t drain;
+    int odd_run;                   // last run (counted from 1) with a non-finite value element among its nodes
     alignas(16) uint32_t mask[TT_MASKS][TT_MASK_WORDS];
     uint32_t tmem;
     int abort_flag;
@@ -165,6 +166,44 @@ __device__ __noinline__ bool tt_rescale(uint32_t o_col, uint32_t s_col, float al
     return true;
 }
 
+// Both bf16 halves, non-finite ones as 0.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+    if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+    if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
+    return v;
+}
+
+// Adds the non-finite value elements of the nodes at positions [from, to) that a row
+// sees to columns [c0, c0 + cols) of its O (times a positive weight they stay what
+// they are).  Read from the pool again, a row per thread of the warp: this is for
+// models that have come apart.
+template <int D>
+__device__ __noinline__ void tt_add_odd(const void* v_cache, int num_blocks, int num_kv_heads, int log2_block, uint32_t o_col,
+                                        int c0, int cols, const int32_t* table, int kvh, const uint32_t* mrow, int words,
+                                        int pre, int from, int to, bool valid) {
+#pragma unroll 1
+    for (int c = c0; c < c0 + cols; c += 32) {
+        float o[32];
+        tmem_load32(o_col + c, o);
+        for (int p = from; p < to; ++p) {
+            if (!valid || !(tree_bits(mrow, words, p - pre) & 1u)) continue;
+            const int b = table[p >> log2_block];
+            if (b < 0 || b >= num_blocks) continue;
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                static_cast<const __nv_bfloat16*>(v_cache) +
+                (((static_cast<size_t>(b) * num_kv_heads + kvh) << log2_block) + (p & ((1 << log2_block) - 1))) * D + c);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t w = v[k], odd = w ^ finite_bf16x2(w);
+                if ((odd & 0xffffu) != 0u) o[2 * k] += bf16_lo(w);
+                if ((odd >> 16) != 0u) o[2 * k + 1] += bf16_hi(w);
+            }
+        }
+        __syncwarp();
+        tmem_store32(o_col + c, o);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(TT_THREADS, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
@@ -180,6 +219,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         sh.abort_flag = 0;
+        sh.odd_run = 0;
         for (int i = 0; i < TT_SLOTS; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 1);
             mbar_init(smem_u32(&sh.empty[i]), 1);
@@ -406,7 +446,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // numbers leave every weight of a row at 1 just as well
         const float sl2 = a.scale_log2 == 0.f ? 1e-37f : a.scale_log2;
         uint32_t ring = 0, tiles = 0, use = 0;    // ring position and tile of the run's start; the stream's steps
+        int run = 0;                              // runs so far
         while (walk.next(a, r)) {
+            ++run;
             const bool two = r.per_tile == 2;
             const int nt = r.t1 - r.t0;
             // Q: one or two tiles of 128 rows; rows past the unit's are zero.  A thread
@@ -465,26 +507,39 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const uint2 in = *reinterpret_cast<const uint2*>(&sh.mask[mi][2 * h]);
                 ready = ready && tt_wait(&sh.s_full[w][use & 1u], (use >> 1) & 1u, abort_flag, a.dev_err);
                 const bool all_in = (in.x & in.y) == 0xffffffffu;
-                if (!all_in) ready = ready && tt_wait(&sh.full[vslot], (vg / TT_SLOTS) & 1u, abort_flag, a.dev_err);
+                const int p0 = (r.t0 + j) * TT_KT + h * TT_HT;
+                const bool every = all_in && p0 + TT_HT <= pre;   // every token seen by every row
+                if (!every) ready = ready && tt_wait(&sh.full[vslot], (vg / TT_SLOTS) & 1u, abort_flag, a.dev_err);
                 if (!__all_sync(FULL_MASK, ready)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after_sync();
-                // value rows of tokens that take no part may hold anything, NaN too:
-                // zero them, so that 0 * V stays 0 (two row tiles share the half:
-                // stream 0's P.V comes first, and its warps do it)
-                if (!all_in && (!two || w == 0)) {
+                // Value rows of tokens that take no part may hold anything, NaN too: zero
+                // them, so that 0 * V stays 0.  A node's non-finite value elements must
+                // not reach the rows that do not see it (weight 0) either: they become
+                // zero, and the epilogue gives them to the rows that do.  (Two row tiles
+                // share the half: stream 0's P.V comes first, and its warps do it.)
+                if (!every && (!two || w == 0)) {
                     uint8_t* vs = smem + Geo::OFF_SLOTS + vslot * Geo::SLOT + h * (Geo::SLOT / 2);
+                    bool odd = false;
                     for (int i = row; i < TT_HT * NH * 8; i += TT_M) {
                         const int tok = i / (NH * 8), ch = i % (NH * 8);
-                        if (!(((tok < 32 ? in.x : in.y) >> (tok & 31)) & 1u))
-                            *reinterpret_cast<uint4*>(vs + (tok / 8) * Geo::GROUP + (ch / 8) * 1024 + (tok % 8) * 128 + (ch % 8) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                        uint4* at = reinterpret_cast<uint4*>(vs + (tok / 8) * Geo::GROUP + (ch / 8) * 1024 + (tok % 8) * 128 + (ch % 8) * 16);
+                        if (!(((tok < 32 ? in.x : in.y) >> (tok & 31)) & 1u)) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (p0 + tok >= pre) {
+                            const uint4 v = *at;
+                            const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+                            if (((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) != 0u) {
+                                *at = f;
+                                odd = true;
+                            }
+                        }
                     }
+                    if (odd) *const_cast<volatile int*>(&sh.odd_run) = run;
                     fence_proxy_async_smem();
                 }
-                const int p0 = (r.t0 + j) * TT_KT + h * TT_HT;
                 if (busy) {
                     const float unseen = sl2 >= 0.f ? NEG_INF : INFINITY;   // times the scale: -inf
                     // One pass over S, 32 columns at a time with the next 32 under way:
@@ -493,7 +548,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     // down: the sum, O, and the step's weights already written.
                     // That is rare after a run's first tiles; a pass of its own for the
                     // maximum took a quarter of the softmax's time.
-                    const bool every = all_in && p0 + TT_HT <= pre;   // every token seen by every row
                     f32x2 sum(0.f, 0.f);
                     uint32_t x[32];
                     tmem_issue32(s_col, x);
@@ -595,6 +649,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 const float f0 = c0 * inv, f1 = c1 * inv;
                 const size_t at = valid ? tree_out_row(a, r.first, r.kvh, r.row0 + R) * D : 0;
                 float4* acc = reinterpret_cast<float4*>(tree_part(a, slot, D)) + R;
+                if (*const_cast<volatile int*>(&sh.odd_run) == run)   // to the stream that counts more
+                    tt_add_odd<D>(a.v_cache, a.num_blocks, a.num_kv_heads, a.log2_block, first + (!two && c1 > c0 ? D : 0),
+                                  col0, cols, a.block_tables + static_cast<size_t>(r.s) * a.max_blocks, r.kvh, mrow,
+                                  a.mask_words32, pre,
+                                  max(max(0, pre), r.t0 * TT_KT), min(r.ctx, r.t1 * TT_KT), valid);
 #pragma unroll 1
                 for (int c = col0; c < col0 + cols; c += 32) {
                     float o[32];

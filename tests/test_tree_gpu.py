@@ -358,3 +358,76 @@ def test_tree_overlapping_ranges_stay_in_bounds(pa):
         out, err = run(pa, step, q, mask, np.array([0, 10, 0, 10, 0, 10, 10], dtype=np.int32))
         assert err == pa.DEVERR_CONTEXT
         assert torch.isfinite(out[:10]).all() and torch.all(out[10:] == -77.0)
+
+
+@pytest.mark.parametrize("case", [([300, 70], [40, 70], 8, 2, 128, 16), ([200], [100], 8, 2, 64, 8), ([64, 33], [9, 5], 4, 4, 64, 4)])
+def test_tree_non_finite_nodes_reach_only_rows_that_see_them(pa, case):
+    """NaN and infinities in K and V of some nodes: rows that do not see such a node are the same bit for bit as
+    without them; rows that see one are non-finite where plain attention is."""
+    ctx, nodes, Hq, Hkv, d, B = case
+    step, q, mask, start = inputs(ctx, nodes, Hq, Hkv, d, B, torch.bfloat16)
+    clean, err = run(pa, step, q, mask, start)
+    assert err == 0
+    words = mask.view(np.uint64)
+    for which, bad_nodes in (("v", [1, nodes[0] - 1]), ("k", [2])):
+        k0, v0 = step.k_cache.clone(), step.v_cache.clone()
+        pool = step.v_cache if which == "v" else step.k_cache
+        for j, value in zip(bad_nodes, (float("nan"), float("inf"))):
+            p = ctx[0] - nodes[0] + j
+            pool[int(step.block_tables[0, p // B]), :, p % B, 5] = value
+        out, err = run(pa, step, q, mask, start)
+        torch.cuda.synchronize()
+        assert err == 0
+        for i in range(q.shape[0]):
+            own = i < nodes[0]
+            sees = [j for j in bad_nodes if own and (int(words[i, j // 64]) >> (j % 64)) & 1]
+            if not sees:
+                assert torch.equal(out[i], clean[i]), (which, i)
+            elif which == "v":
+                assert not torch.isfinite(out[i, :, 5]).any()
+                others = [c for c in range(d) if c != 5]
+                assert torch.equal(out[i][:, others], clean[i][:, others])
+                if len(sees) == 1 and sees[0] == bad_nodes[1]:
+                    assert torch.all(out[i, :, 5] == float("inf"))
+            else:
+                assert torch.isnan(out[i]).all()
+        step.k_cache.copy_(k0)
+        step.v_cache.copy_(v0)
+
+
+def test_tree_blocks_past_four_gigabytes(pa):
+    """The pool's last blocks, element offsets above 2^32."""
+    Hkv, B, d = 8, 16, 128
+    NB = (1 << 32) // (Hkv * B * d) + 64
+    kc = torch.empty(NB, Hkv, B, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    ids = [NB - 1, 3, NB - 7, NB - 40]
+    for b in ids:
+        kc[b].normal_()
+        vc[b].normal_()
+    ctx, n = 60, 11
+    parents = [-1, 0, 0, 1, 1, 2, 2, 3, 4, 5, 6]
+    mask = pa.tree_mask(parents).cuda()
+    q = torch.randn(n, 16, d, device="cuda").to(torch.bfloat16)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.tree_decode(out, q, kc, vc, i32([ids]), i32([ctx]), i32([0, n]), mask, d ** -0.5, dev_err=err)
+    small_k, small_v = torch.stack([kc[b] for b in ids]), torch.stack([vc[b] for b in ids])
+    ref = oracle.tree_attention(f64(q), f64(small_k), f64(small_v), [[0, 1, 2, 3]], [ctx], [0, n],
+                                mask.tolist(), d ** -0.5)
+    assert int(err.item()) == 0
+    close(out, ref, torch.bfloat16)
+    # decode with totals and a move inside the same blocks
+    w = torch.zeros(1, Hkv, 64, device="cuda")
+    dout = torch.empty(1, 16, d, dtype=torch.float32, device="cuda")
+    pa.decode_weights(dout, w, q[:1].contiguous(), kc, vc, i32([ids]), i32([ctx]), d ** -0.5, dev_err=err)
+    exact = oracle.attention_weights(f64(q[:1]), f64(small_k), [[0, 1, 2, 3]], [ctx], d ** -0.5)[0]
+    assert np.abs(f64(w[0, :, :ctx]) - exact).max() <= 6e-4 * exact.max()
+    keep = [1, 17, 30, 40, 59]
+    pa.compact(kc, vc, i32([ids]), i32([ids]), i32([[keep]]), i32([len(keep)]), dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for j, p in enumerate(keep):
+        assert torch.equal(kc[ids[0], :, j], small_k[p // B, :, p % B])
+        assert torch.equal(vc[ids[0], :, j], small_v[p // B, :, p % B])
