@@ -9,6 +9,7 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_host.h"
@@ -120,14 +121,18 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
                 sK[(c + 2) * TS_PAD + tok] = k4.z;
                 sK[(c + 3) * TS_PAD + tok] = k4.w;
             }
+            int odd = 0;
             for (int i = tid; i < TS_KT * (D / 4); i += TS_THREADS) {
                 const int tok = i / (D / 4), c = i % (D / 4) * 4;
                 const int at = s_row[tok];
                 float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);   // tokens that take no part: 0 * 0
                 if (at >= 0) v4 = load4<T>(vc + static_cast<size_t>(at) * D + c);
+                // a node's non-finite value must not meet the zero weight of a row that
+                // does not see it
+                if (p0 + tok >= pre) odd |= !(isfinite(v4.x) && isfinite(v4.y) && isfinite(v4.z) && isfinite(v4.w));
                 *reinterpret_cast<float4*>(sV + tok * D + c) = v4;
             }
-            __syncthreads();
+            const bool guarded = __syncthreads_or(odd);
             float x[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -177,26 +182,26 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
                     make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
             }
             __syncwarp();   // a row's 16 threads share a warp
+            auto add_values = [&](auto skip_zero) {
 #pragma unroll 2
-            for (int tok = 0; tok < TS_KT; tok += 4) {
-                float p[4][4];
+                for (int tok = 0; tok < TS_KT; tok += 4) {
+                    float p[4][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 v = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * TS_PAD + tok);
-                    p[i][0] = v.x;
-                    p[i][1] = v.y;
-                    p[i][2] = v.z;
-                    p[i][3] = v.w;
-                }
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 v = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * TS_PAD + tok);
+                        p[i][0] = v.x;
+                        p[i][1] = v.y;
+                        p[i][2] = v.z;
+                        p[i][3] = v.w;
+                    }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                    for (int j = 0; j < OC; j += 4) {
-                        const float4 v = *reinterpret_cast<const float4*>(sV + (tok + k) * D + 16 * j + 4 * tx);
+                        for (int j = 0; j < OC; j += 4) {
+                            const float4 v = *reinterpret_cast<const float4*>(sV + (tok + k) * D + 16 * j + 4 * tx);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // a token the row does not see adds nothing, whatever its value
-                            if (p[i][k] != 0.f) {
+                            for (int i = 0; i < 4; ++i) {
+                                if (decltype(skip_zero)::value && p[i][k] == 0.f) continue;
                                 o[i][j + 0] = fmaf(p[i][k], v.x, o[i][j + 0]);
                                 o[i][j + 1] = fmaf(p[i][k], v.y, o[i][j + 1]);
                                 o[i][j + 2] = fmaf(p[i][k], v.z, o[i][j + 2]);
@@ -205,7 +210,11 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
                         }
                     }
                 }
-            }
+            };
+            if (guarded)
+                add_values(std::true_type());
+            else
+                add_values(std::false_type());
         }
         const bool whole = r.t0 == 0 && r.t1 == r.nt;
         const int slot = 2 * blockIdx.x + (r.starts ? 0 : 1);
