@@ -1307,27 +1307,15 @@ __global__ void __launch_bounds__(128, 4) attend_f32_logits_kernel(const DecodeA
 // of the output and sum the partitions in order.
 constexpr int REDUCE_HEADS_MAX_PARTS = 32;
 
+// The merge of one head, by a warp.
 template <int D>
-__global__ void __launch_bounds__(128) reduce_heads_kernel(const DecodeArgs a) {
+__device__ __forceinline__ void reduce_head_warp(const DecodeArgs& a, int s, int head) {
     constexpr int C4 = D / 4, SUB = 32 / C4, U = 8;   // SUB lanes groups split the partitions
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quads = (a.num_heads + 3) / 4;
-    const int s = blockIdx.x / quads, head = (blockIdx.x - (blockIdx.x / quads) * quads) * 4 + warp;
-    if (head < a.num_heads) {   // the lines this warp reads first, while attend finishes: the length,
-        // the (max, sum) pairs and the first two partials (every row the kernel merges has at least two;
-        // how many more is known only from the length)
-        const size_t r = static_cast<size_t>(s) * a.num_heads + head;
-        if (lane == 0) prefetch_l2(a.context_lens + s);
-        if (lane == 1) prefetch_l2(a.ws_ml + r * a.max_parts);
-        constexpr int LINES = D / 32;   // 128-byte lines of one partial
-        const int pp = lane / LINES;
-        if (pp < 2 && pp < a.max_parts) prefetch_l2(a.ws_acc + (r * a.max_parts + pp) * D + (lane % LINES) * 32);
-    }
-    pdl_wait();
-    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    if (head >= a.num_heads) return;
     const int ctx = clamp_context(a.context_lens[s], a.cap);
     const int nparts = (ctx + a.partition_size - 1) / a.partition_size;
-    if (nparts <= 1 || head >= a.num_heads) return;   // single partitions are written by attend
+    if (nparts <= 1) return;   // single partitions are written by attend
     const size_t row = static_cast<size_t>(s) * a.num_heads + head;
     const int c4 = lane % C4, sub = lane / C4;
     const float4* accp = reinterpret_cast<const float4*>(a.ws_acc + row * a.max_parts * D) + c4;
@@ -1385,6 +1373,26 @@ __global__ void __launch_bounds__(128) reduce_heads_kernel(const DecodeArgs a) {
                 static_cast<__nv_bfloat16*>(a.out)[row * D + 4 * c4 + k] = __float2bfloat16_rn(val);
         }
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) reduce_heads_kernel(const DecodeArgs a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quads = (a.num_heads + 3) / 4;
+    const int s = blockIdx.x / quads, head = (blockIdx.x - (blockIdx.x / quads) * quads) * 4 + warp;
+    if (head < a.num_heads) {   // the lines this warp reads first, while attend finishes: the length,
+        // the (max, sum) pairs and the first two partials (every row the kernel merges has at least two;
+        // how many more is known only from the length)
+        const size_t r = static_cast<size_t>(s) * a.num_heads + head;
+        if (lane == 0) prefetch_l2(a.context_lens + s);
+        if (lane == 1) prefetch_l2(a.ws_ml + r * a.max_parts);
+        constexpr int LINES = D / 32;   // 128-byte lines of one partial
+        const int pp = lane / LINES;
+        if (pp < 2 && pp < a.max_parts) prefetch_l2(a.ws_acc + (r * a.max_parts + pp) * D + (lane % LINES) * 32);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    reduce_head_warp<D>(a, s, head);
 }
 
 // Longer contexts: one CTA of REDUCE_PARTS_THREADS per (seq, head).  The
@@ -1477,7 +1485,9 @@ __global__ void __launch_bounds__(REDUCE_PARTS_THREADS, 4) reduce_parts_kernel(c
 // x from ws_x, (M_n, L_n) the merged (max, sum) of head n's partitions.
 // A weight needs the whole context's sum, which no partition knows while it
 // runs: hence the logits' round trip, 8 * group bytes per token and kv head
-// next to the 2 * d * e of its K and V, mostly through L2.
+// next to the 2 * d * e of its K and V, mostly through L2.  The first merge_ctas
+// CTAs merge the output's partitions meanwhile (contexts of at most
+// REDUCE_HEADS_MAX_PARTS partitions): a launch less, 2 us of a short step's 21.
 // ---------------------------------------------------------------------------
 
 constexpr int WEIGHTS_THREADS = 256;
@@ -1485,14 +1495,22 @@ constexpr int WEIGHTS_PER_THREAD = 2;
 constexpr int WEIGHTS_TOKENS = WEIGHTS_THREADS * WEIGHTS_PER_THREAD;   // tokens per CTA
 constexpr int WEIGHTS_MAX_GROUP = 256;   // query heads per kv head (their coefficients sit in shared memory)
 
-__global__ void __launch_bounds__(WEIGHTS_THREADS) weights_kernel(const DecodeArgs a, int chunks) {
+template <int D>
+__global__ void __launch_bounds__(WEIGHTS_THREADS) weights_kernel(const DecodeArgs a, int chunks, int merge_ctas) {
     __shared__ float2 s_ml[WEIGHTS_MAX_GROUP];   // (max, 1 / sum) of each query head
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.x / chunks;         // s * num_kv_heads + kvh
-    const int t0 = (blockIdx.x - row * chunks) * WEIGHTS_TOKENS;
+    const int block = static_cast<int>(blockIdx.x) - merge_ctas;
+    const int row = block / chunks;              // s * num_kv_heads + kvh
+    const int t0 = (block - row * chunks) * WEIGHTS_TOKENS;
     const int s = row / a.num_kv_heads, kvh = row - s * a.num_kv_heads, G = a.group;
     pdl_wait();
     pdl_launch_dependents();
+    if (block < 0) {
+        const long long head_row = static_cast<long long>(blockIdx.x) * (WEIGHTS_THREADS / 32) + warp;
+        const int hs = static_cast<int>(head_row / a.num_heads);
+        if (hs < a.num_seqs) reduce_head_warp<D>(a, hs, static_cast<int>(head_row - static_cast<long long>(hs) * a.num_heads));
+        return;
+    }
     const int ctx = clamp_context(a.context_lens[s], a.cap);
     if (t0 >= ctx) return;
     const int nparts = (ctx + a.partition_size - 1) / a.partition_size;
@@ -1743,7 +1761,7 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
     if (static_cast<long long>(num_seqs) * max_parts > (INT_MAX >> ITEM_LOW_BITS)) return PA_ERR_UNSUPPORTED;
     if (weights != nullptr) {
         if (num_heads / num_kv_heads > WEIGHTS_MAX_GROUP ||
-            static_cast<long long>(num_seqs) * num_kv_heads * (cap / WEIGHTS_TOKENS + 1) > INT_MAX)
+            static_cast<long long>(num_seqs) * num_kv_heads * (cap / WEIGHTS_TOKENS + 1) + static_cast<long long>(num_seqs) * num_heads > INT_MAX)
             return PA_ERR_UNSUPPORTED;
         if (!weights->out || !aligned_to(weights->out, 4) || (weights->in && !aligned_to(weights->in, 4)) ||
             (weights->lens && !aligned_to(weights->lens, 4)) || weights->stride < cap)
@@ -1824,7 +1842,9 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
         const int rc = weights != nullptr ? launch_attend<true>(a, dtype, st) : launch_attend<false>(a, dtype, st);
         if (rc != PA_OK) return rc;
     }
-    if ((phases & PA_PHASE_REDUCE) && max_parts > 1) {
+    // pa_decode_weights merges few partitions in its last launch
+    const bool merge_late = weights != nullptr && max_parts > 1 && max_parts <= REDUCE_HEADS_MAX_PARTS;
+    if ((phases & PA_PHASE_REDUCE) && max_parts > 1 && !merge_late) {
         cudaError_t e;
         if (max_parts <= REDUCE_HEADS_MAX_PARTS) {
             const long long ctas = static_cast<long long>(num_seqs) * ((num_heads + 3) / 4);
@@ -1842,9 +1862,15 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
     }
     if (weights != nullptr) {
         const int chunks = (a.cap + WEIGHTS_TOKENS - 1) / WEIGHTS_TOKENS;
-        const long long ctas = static_cast<long long>(num_seqs) * num_kv_heads * chunks;
-        if (launch_status(launch_pdl(weights_kernel, dim3(static_cast<unsigned>(ctas)), dim3(WEIGHTS_THREADS), 0, st, a,
-                                     chunks)) != PA_OK)
+        const long long heads = static_cast<long long>(num_seqs) * num_heads;
+        const long long merge = merge_late ? (heads + WEIGHTS_THREADS / 32 - 1) / (WEIGHTS_THREADS / 32) : 0;
+        const long long ctas = merge + static_cast<long long>(num_seqs) * num_kv_heads * chunks;
+        const dim3 grid(static_cast<unsigned>(ctas));
+        const cudaError_t e =
+            head_dim == 128
+                ? launch_pdl(weights_kernel<128>, grid, dim3(WEIGHTS_THREADS), 0, st, a, chunks, static_cast<int>(merge))
+                : launch_pdl(weights_kernel<64>, grid, dim3(WEIGHTS_THREADS), 0, st, a, chunks, static_cast<int>(merge));
+        if (launch_status(e) != PA_OK)
             return PA_ERR_CUDA;
     }
     return PA_OK;
