@@ -332,7 +332,7 @@ PA_API int pa_decode_noalloc(void* out, pa_dtype out_dtype, const void* q, const
  * below zero do not exist.  Other arguments and errors as for pa_decode.
  * Arithmetic: as for pa_decode.  The work is cut over the GPU by the whole batch, so the same
  * call gives the same bits every time, but a sequence's rounding may differ in another batch.
- * On bf16 pools with block_size 8, 16 or 32 (pa_tree_uses_tensor_cores) the products run as
+ * On bf16 pools (pa_tree_uses_tensor_cores) the products run as
  * tcgen05 MMAs over tiles of 128 query rows; elsewhere on the CUDA cores in fp32.  A
  * non-finite K or V of a node reaches the rows that see it and no others.
  * Launches two kernels (attention, join) on `stream`.  Calls that may overlap in time need

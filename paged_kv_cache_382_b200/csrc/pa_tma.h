@@ -63,4 +63,20 @@ inline bool encode_block_map(CUtensorMap* m, const void* pool, int num_blocks, i
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same for blocks of four tokens, half a group: one box is a 64-column part of
+// a block, and two blocks share a group.  (The 128-byte swizzle goes by the address
+// in shared memory, so the second half of a group is swizzled as its rows 4 to 7.)
+inline bool encode_half_group_map(CUtensorMap* m, const void* pool, int num_blocks, int Hkv, int D) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+    const cuuint64_t dims[4] = {64u, 4u, static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(num_blocks) * Hkv};
+    const cuuint64_t strides[3] = {row, 128u, 4 * row};
+    const cuuint32_t box[4] = {64u, 4u, 1u, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pa

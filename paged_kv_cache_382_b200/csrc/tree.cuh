@@ -1,5 +1,5 @@
 // tree.cuh -- attention of drafted tokens over a paged cache (pa_tree_decode):
-// what its two attend kernels share (tree_decode.cu on the CUDA cores, any pool;
+// what its two attend kernels share (tree_decode.cu on the CUDA cores, fp32 pools;
 // tree_tc.cu on the tensor cores, bf16 pools).
 //
 // What is computed: new token ("node") i of sequence s, one of n_s, sees every

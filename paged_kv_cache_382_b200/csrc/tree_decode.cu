@@ -1,7 +1,6 @@
 // tree_decode.cu -- pa_tree_decode: attention of a tree of drafted tokens over
 // a paged cache.  The entry point, the attend kernel on the CUDA cores (fp32
-// pools, and bf16 pools of 4-token blocks), the join of cut units, and the
-// host-side construction of masks from parents (pa_tree_mask).  tree.cuh says
+// pools), the join of cut units, and the host-side construction of masks from parents (pa_tree_mask).  tree.cuh says
 // what is computed and how the work is cut.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -39,19 +38,9 @@ constexpr int tree_simt_smem() {
     return (2 * D * TS_PAD + TS_KT * D) * 4;
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-    return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
-}
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs a) {
     constexpr int OC = D / 16;   // output columns per thread
     extern __shared__ __align__(16) uint8_t smem_dyn[];
@@ -61,9 +50,9 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
     float* sP = sK;                                   // [TS_ROWS][TS_PAD], once S is complete
     __shared__ int s_row[TS_KT];                      // pool row of each token of the tile, or -1
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const T* q = static_cast<const T*>(a.q);
-    const T* kc = static_cast<const T*>(a.k_cache);
-    const T* vc = static_cast<const T*>(a.v_cache);
+    const float* q = static_cast<const float*>(a.q);
+    const float* kc = static_cast<const float*>(a.k_cache);
+    const float* vc = static_cast<const float*>(a.v_cache);
     pdl_wait();
     pdl_launch_dependents();
     TreeWalker<TS_ROWS, 1, TS_KT> walk;
@@ -77,7 +66,7 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
         for (int i = tid; i < TS_ROWS * (D / 4); i += TS_THREADS) {
             const int row = i % TS_ROWS, c = i / TS_ROWS * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row < r.rows) v = load4<T>(q + tree_out_row(a, r.first, r.kvh, r.row0 + row) * D + c);
+            if (row < r.rows) v = load4(q + tree_out_row(a, r.first, r.kvh, r.row0 + row) * D + c);
             sQ[(c + 0) * TS_PAD + row] = v.x;
             sQ[(c + 1) * TS_PAD + row] = v.y;
             sQ[(c + 2) * TS_PAD + row] = v.z;
@@ -115,7 +104,7 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
                 const int tok = i % TS_KT, c = i / TS_KT * 4;
                 const int at = s_row[tok];
                 float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (at >= 0) k4 = load4<T>(kc + static_cast<size_t>(at) * D + c);
+                if (at >= 0) k4 = load4(kc + static_cast<size_t>(at) * D + c);
                 sK[(c + 0) * TS_PAD + tok] = k4.x;
                 sK[(c + 1) * TS_PAD + tok] = k4.y;
                 sK[(c + 2) * TS_PAD + tok] = k4.z;
@@ -126,7 +115,7 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
                 const int tok = i / (D / 4), c = i % (D / 4) * 4;
                 const int at = s_row[tok];
                 float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);   // tokens that take no part: 0 * 0
-                if (at >= 0) v4 = load4<T>(vc + static_cast<size_t>(at) * D + c);
+                if (at >= 0) v4 = load4(vc + static_cast<size_t>(at) * D + c);
                 // a node's non-finite value must not meet the zero weight of a row that
                 // does not see it
                 if (p0 + tok >= pre) odd |= !(isfinite(v4.x) && isfinite(v4.y) && isfinite(v4.z) && isfinite(v4.w));
@@ -226,16 +215,9 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
                 const size_t at = tree_out_row(a, r.first, r.kvh, r.row0 + row) * D;
                 const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
 #pragma unroll
-                for (int j = 0; j < OC; j += 4) {
-                    const int c = 16 * j + 4 * tx;
-                    if (a.out_f32)
-                        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + c) =
-                            make_float4(o[i][j] * inv, o[i][j + 1] * inv, o[i][j + 2] * inv, o[i][j + 3] * inv);
-                    else
-                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at + c) =
-                            make_uint2(pack_bf16(o[i][j] * inv, o[i][j + 1] * inv),
-                                       pack_bf16(o[i][j + 2] * inv, o[i][j + 3] * inv));
-                }
+                for (int j = 0; j < OC; j += 4)
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 16 * j + 4 * tx) =
+                        make_float4(o[i][j] * inv, o[i][j + 1] * inv, o[i][j + 2] * inv, o[i][j + 3] * inv);
             } else {
                 float4* acc = reinterpret_cast<float4*>(tree_part(a, slot, D));
 #pragma unroll
@@ -248,10 +230,10 @@ __global__ void __launch_bounds__(TS_THREADS, 2) tree_simt_kernel(const TreeArgs
     }
 }
 
-template <int D, typename T>
+template <int D>
 int launch_tree_simt(const TreeArgs& a, int ctas, cudaStream_t st) {
     static KernelSlot slot;
-    auto kern = tree_simt_kernel<D, T>;
+    auto kern = tree_simt_kernel<D>;
     if (prepare_kernel(slot, reinterpret_cast<const void*>(kern), TS_THREADS, tree_simt_smem<D>()) <= 0) return PA_ERR_CUDA;
     return launch_status(launch_pdl(kern, dim3(ctas), dim3(TS_THREADS), tree_simt_smem<D>(), st, a));
 }
@@ -483,11 +465,8 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
     int rc;
     if (tc)
         rc = launch_tree_tc(a, head_dim, ctas, st);
-    else if (dtype == PA_F32)
-        rc = head_dim == 128 ? launch_tree_simt<128, float>(a, ctas, st) : launch_tree_simt<64, float>(a, ctas, st);
     else
-        rc = head_dim == 128 ? launch_tree_simt<128, __nv_bfloat16>(a, ctas, st)
-                             : launch_tree_simt<64, __nv_bfloat16>(a, ctas, st);
+        rc = head_dim == 128 ? launch_tree_simt<128>(a, ctas, st) : launch_tree_simt<64>(a, ctas, st);
     if (rc != PA_OK || ctas < 2) return rc;
     const dim3 grid(ctas - 1, (a.part_rows + TJ_ROWS - 1) / TJ_ROWS);
     return launch_status(head_dim == 128 ? launch_pdl(tree_join_kernel<128>, grid, dim3(TJ_THREADS), 0, st, a, ctas)

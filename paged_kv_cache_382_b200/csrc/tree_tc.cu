@@ -25,7 +25,10 @@
 // K and V tiles go through one ring of five 32 KB slots in the order K0 V0 K1
 // V1 ...; a K slot is free again once its S are done, so up to 160 KB are in
 // flight or in use.  Two loader warps, one for K and one for V, run ahead into
-// the CTA's next runs.  One bulk copy brings a whole block.  Next to busy softmax
+// the CTA's next runs.  One bulk copy brings a whole block, or 64
+// columns of a block of four tokens (64 copies per slot at d = 128, which bound the
+// kernel: 64 130 tokens of one sequence, 40 / 8 heads, take 167 us; 1155 us on the
+// CUDA cores).  Next to busy softmax
 // warps a loader needs 2150 cycles for a slot of 8-token blocks (460 alone): one
 // warp for both pools held an SM at 22 GB/s.
 //
@@ -99,6 +102,17 @@ struct TreeShared {
     uint32_t tmem;
     int abort_flag;
 };
+
+// Bulk tensor copy of box (0, 0, part, block) of a map of half groups.
+__device__ __forceinline__ void tt_load_half_group_elected(uint32_t elected, uint32_t dst, const void* tensor_map, uint32_t bar,
+                                                           int part, int block) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tensor_map)), "r"(bar), "r"(0), "r"(part), "r"(block), "r"(elected)
+        : "memory");
+}
 
 // Bounds a loop of polls: true once WAIT_LIMIT_NS have passed since the first
 // of them.  The global timer is slow to read: only every 256th poll looks.
@@ -256,7 +270,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         uint32_t ring = is_v ? 1 : 0, tiles = 0;   // ring position and tiles passed so far
         bool ok = true;
         const uint32_t leader = elect_one();
-        const int per = TT_KT / B;      // blocks of a tile: one lane each (at most 16)
+        const int per = TT_KT / B;      // blocks of a tile: one lane each
         const uint32_t slots = __shfl_sync(FULL_MASK, sSlots, 0);
         while (ok && walk.next(a, r)) {
             if (r.starts && !is_v && lane == 0) tree_record(a, r);
@@ -273,7 +287,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 if (bad) flag_error(a.dev_err, PA_DEVERR_BLOCK_ID);
                 const uint32_t valid = __ballot_sync(FULL_MASK, here);
                 const uint32_t bytes = __popc(valid) * NH * static_cast<uint32_t>(B) * 128u;
-                const int group = here ? (entry * a.num_kv_heads + r.kvh) * (B / 8) : 0;
+                const int group = here ? (entry * a.num_kv_heads + r.kvh) * (B < 8 ? 1 : B / 8) : 0;
                 const uint32_t slot = ring % TT_SLOTS;
                 bool w = true;
                 if (ring >= TT_SLOTS) w = tt_wait(&sh.empty[slot], ((ring / TT_SLOTS) - 1) & 1u, abort_flag, a.dev_err);
@@ -289,8 +303,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
                     for (int u = 0; u < 4; ++u) at[u] = __shfl_sync(FULL_MASK, group, i + u);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        tma_load_group_elected(leader & (valid >> (i + u)), dst + (i + u) * (B / 8) * Geo::GROUP, map, bar, at[u]);
+                    for (int u = 0; u < 4; ++u) {
+                        if (B >= 8) {
+                            tma_load_group_elected(leader & (valid >> (i + u)), dst + (i + u) * (B / 8) * Geo::GROUP, map, bar, at[u]);
+                            continue;
+                        }
+#pragma unroll
+                        for (int h = 0; h < NH; ++h)
+                            tt_load_half_group_elected(leader & (valid >> (i + u)),
+                                                       dst + ((i + u) >> 1) * Geo::GROUP + h * 1024 + (u & 1) * 512, map, bar, h, at[u]);
+                    }
                 }
                 if (!is_v) {
                     // tokens of the tile that take part: in the context and in a valid
@@ -701,9 +723,11 @@ template <int D>
 int launch(const TreeArgs& a, int ctas, cudaStream_t st) {
     static KernelSlot slot;
     CUtensorMap tk, tv;
-    if (!encode_block_map(&tk, a.k_cache, a.num_blocks, a.num_kv_heads, a.block_size, D) ||
-        !encode_block_map(&tv, a.v_cache, a.num_blocks, a.num_kv_heads, a.block_size, D))
-        return PA_ERR_CUDA;
+    auto encode = [&](CUtensorMap* m, const void* pool) {
+        return a.block_size < 8 ? encode_half_group_map(m, pool, a.num_blocks, a.num_kv_heads, D)
+                                : encode_block_map(m, pool, a.num_blocks, a.num_kv_heads, a.block_size, D);
+    };
+    if (!encode(&tk, a.k_cache) || !encode(&tv, a.v_cache)) return PA_ERR_CUDA;
     const int smem = TreeGeom<D>::BYTES + 1024;
     auto kern = tree_tc_kernel<D>;
     if (prepare_kernel(slot, reinterpret_cast<const void*>(kern), TT_THREADS, smem) <= 0) return PA_ERR_CUDA;
@@ -713,7 +737,7 @@ int launch(const TreeArgs& a, int ctas, cudaStream_t st) {
 }  // namespace
 
 bool tree_tc_eligible(pa_dtype dtype, int block_size) {
-    return dtype == PA_BF16 && (block_size == 8 || block_size == 16 || block_size == 32);
+    return dtype == PA_BF16 && (block_size == 4 || block_size == 8 || block_size == 16 || block_size == 32);
 }
 
 int tree_tc_rows() { return TT_ROWS; }

@@ -103,6 +103,8 @@ CASES = [
     ([65, 260], [2, 37], 16, 2, 128, 16),
     ([2100], [17], 8, 8, 64, 32),
     ([90, 17], [9, 4], 8, 4, 64, 4),
+    ([301, 1023, 4], [17, 40, 3], 32, 8, 128, 4),
+    ([130, 2055], [45, 6], 12, 2, 64, 4),
 ]
 
 
@@ -111,7 +113,7 @@ CASES = [
 def test_tree_matches_oracle(pa, case, dtype):
     ctx, nodes, Hq, Hkv, d, B = case
     step, q, mask, start = inputs(ctx, nodes, Hq, Hkv, d, B, dtype)
-    assert pa.tree_uses_tensor_cores(dtype, B) == (dtype == torch.bfloat16 and B >= 8)
+    assert pa.tree_uses_tensor_cores(dtype, B) == (dtype == torch.bfloat16)
     out, err = run(pa, step, q, mask, start)
     assert err == 0
     close(out, reference(step, q, mask, start), dtype)
