@@ -243,6 +243,9 @@ int append_tokens(pa_block_manager* m, Sequence& sq, const int32_t* token_ids, i
                 sq.table[logical] = fresh;
                 b = fresh;
             }
+            // Cached still where a cut ended inside a full block that others held then: this
+            // slot is about to hold another token.
+            m->evict(b);
         }
         const int32_t b = sq.table[logical];
         slots[i] = static_cast<int64_t>(b) * B + off;
@@ -372,7 +375,8 @@ extern "C" int pa_bm_compact(pa_block_manager* m, int num_seqs, const int64_t* s
             m->decref(sq.table.back());
             sq.table.pop_back();
         }
-        // a cut inside a full block: its later slots will be written again
+        // a cut inside a full block: its later slots will be written again (where others hold
+        // it still, the first append that finds it unshared evicts it)
         if (num_tokens[k] % B != 0 && m->ref_cnt[sq.table.back()] == 1) m->evict(sq.table.back());
         sq.num_tokens = num_tokens[k];
         if (m->prefix_cache && sq.keyed) rekey(m, sq, unchanged[k], num_tokens[k], ids);
