@@ -371,7 +371,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             tmem_fence_after_sync();
             // Step i of the run: stream i % 2, its step base + i / 2, whose parity is
             // the buffer and whose half is the buffer's phase.  S(i) needs its K and
-            // P.V(i - 4) done with the buffer; P.V(i) needs its weights and its V.
+            // P.V(i - 4) done with the buffer; P.V(i) needs its weights and its V.  The
+            // first stream to end, whose last P.V is steps - 2, writes the next run's Q
+            // over both tiles: that P.V comes after the other stream's last S (whose K
+            // is in the same tile), so that its commit stands for both.
             // Each goes in order; the barriers are tested without blocking.
             int ns = 0, no = 0;
             bool k_here = false, v_here = false;   // the slot's copy was seen to have landed
@@ -404,7 +407,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         progressed = true;
                     }
                 }
-                if (no < ns) {
+                if (no < ns && (no + 2 != steps || ns == steps)) {
                     const uint32_t w = no & 1, use = base + (no >> 1), buf = use & 1u;
                     if (passed(bar_at(&sh.p_full[0][0], 2 * w + buf), (use >> 1) & 1u) &&
                         (v_here || (v_here = passed(bar_at(sh.full, v_slot), v_phase)))) {
