@@ -658,6 +658,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                 named_barrier_sync(TT_ML_BARRIER, TT_SOFTMAX);
                 tmem_fence_after_sync();
                 const float2 x0 = ml[row], x1 = ml[TT_M + row];
+                // read by all before a warp without rows, which has no epilogue, writes the
+                // next run's Q there
+                named_barrier_sync(TT_ML_BARRIER, TT_SOFTMAX);
                 M = fmaxf(x0.x, x1.x);
                 c0 = M == NEG_INF ? 0.f : exp2_approx(x0.x - M);
                 c1 = M == NEG_INF ? 0.f : exp2_approx(x1.x - M);

@@ -3,25 +3,35 @@
 The kernel (csrc/tree_tc.cu) gives its two streams of softmax warps two tiles of query rows in shared
 memory.  Before a run both streams write their share of the run's Q (both tiles for more than 128 rows,
 else tile 0), a named barrier tells the MMA warp, and the S products read the tiles until the last of
-them has finished.  Loaders, barriers and clock are those of the models beside it; checked here, under
-random timing, is that every S product finds its run's Q in its tile when it is issued and when it has
-finished.  A planted mistake must be caught: a stream's last P.V that may be issued before the other
-stream's last S (the stream then goes on to the next run's Q while that S still reads).
+them has finished.  In a run of one tile the streams exchange their (max, sum) through tile 1.  Loaders,
+barriers and clock are those of the models beside it; checked here, under random timing, is that
+
+* every S product finds its run's Q in its tile when it is issued and when it has finished, and
+* both streams find this run's (max, sum) when they read the exchange.
+
+Planted mistakes must be caught: a stream's last P.V that may be issued before the other stream's last S (the
+stream then goes on to the next run's Q while that S still reads), and an exchange without a barrier
+behind its reads.
 """
 
 import random
+
+import pytest
 
 from test_tree_protocol_model import SLOTS, TreeSim, loader, random_runs
 
 
 class TileSim(TreeSim):
-    def __init__(self, seed, last_pv_first=False):
+    def __init__(self, seed, last_pv_first=False, unguarded_exchange=False):
         super().__init__(seed)
-        self.last_pv_first = last_pv_first
+        self.last_pv_first, self.unguarded_exchange = last_pv_first, unguarded_exchange
         self.q = [[None, None], [None, None]]     # [tile][the stream that writes this half of its rows]
+        self.exchange = [None, None]              # (max, sum) of each stream, over tile 1
 
     def write_q(self, tile, stream, run):
         self.q[tile][stream] = run
+        if tile == 1:
+            self.exchange = [None, None]
 
     def check_q(self, tile, run):
         if self.q[tile] != [run, run]:
@@ -83,7 +93,13 @@ def softmax(sim, runs, w):
         while not sim.o_done[w][(use - 1) & 1].passed((use - 1) >> 1):
             yield
         if not two:
-            yield "exchange"      # of the streams' (max, sum)
+            sim.exchange[w] = r
+            yield "exchange"
+            yield from sim.pause(4)
+            if sim.exchange != [r, r]:
+                raise AssertionError("the exchanged (max, sum) was overwritten before it was read")
+            if not sim.unguarded_exchange:
+                yield "exchange"
         yield from sim.pause(6 if sim.rng.random() < 0.5 else 0)   # epilogue; a warp without rows has none
 
 
@@ -119,17 +135,18 @@ def run(runs, seed, max_steps=200000, **planted):
     return False
 
 
-def test_every_run_completes_on_its_own_q():
+def test_every_run_completes_on_its_own_q_and_exchange():
     for seed in range(400):
         assert run(random_runs(random.Random(seed)), seed), f"deadlock, seed {seed}"
 
 
-def test_planted_mistake_is_caught():
+@pytest.mark.parametrize("planted,what", [(dict(last_pv_first=True), "S of run"), (dict(unguarded_exchange=True), "exchanged")])
+def test_planted_mistakes_are_caught(planted, what):
     caught = 0
     for seed in range(400):
         try:
-            assert run(random_runs(random.Random(seed)), seed, last_pv_first=True)
+            assert run(random_runs(random.Random(seed)), seed, **planted)
         except AssertionError as e:
-            assert "S of run" in str(e)
+            assert what in str(e)
             caught += 1
     assert caught > 0
