@@ -366,7 +366,8 @@ struct TreeWs {
 inline TreeWs tree_ws(long long num_tokens, int num_heads, int head_dim) {
     TreeWs w;
     const long long rows = num_tokens * num_heads;   // no unit has more
-    w.tc_rows = static_cast<int>(rows < tree_tc_rows() ? rows : tree_tc_rows());
+    // on the tensor cores a row of every stream: both may hold the same rows
+    w.tc_rows = static_cast<int>(2 * rows < tree_tc_rows() ? 2 * rows : tree_tc_rows());
     w.simt_rows = static_cast<int>(rows < TS_ROWS ? rows : TS_ROWS);
     const size_t tc = 2ull * TREE_TC_CTAS * w.tc_rows, simt = 2ull * TREE_SIMT_CTAS * w.simt_rows;
     const size_t most = tc > simt ? tc : simt;
@@ -468,7 +469,9 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
     else
         rc = head_dim == 128 ? launch_tree_simt<128>(a, ctas, st) : launch_tree_simt<64>(a, ctas, st);
     if (rc != PA_OK || ctas < 2) return rc;
-    const dim3 grid(ctas - 1, (a.part_rows + TJ_ROWS - 1) / TJ_ROWS);
+    const long long rows = static_cast<long long>(num_tokens) * num_heads;   // no unit has more
+    const int unit_rows = rows < a.part_rows ? static_cast<int>(rows) : a.part_rows;
+    const dim3 grid(ctas - 1, (unit_rows + TJ_ROWS - 1) / TJ_ROWS);
     return launch_status(head_dim == 128 ? launch_pdl(tree_join_kernel<128>, grid, dim3(TJ_THREADS), 0, st, a, ctas)
                                          : launch_pdl(tree_join_kernel<64>, grid, dim3(TJ_THREADS), 0, st, a, ctas));
 }

@@ -70,6 +70,13 @@ constexpr int TT_TMEM_COLS = 512;
 constexpr int TT_Q_BARRIER = 1;         // Q in shared memory, O read: softmax + MMA warps
 constexpr int TT_ML_BARRIER = 2;        // the streams' (max, sum) exchanged: softmax warps
 constexpr int TT_MASK_WORDS = TT_KT / 32;
+// Steps whose P.V meet in one accumulator.  An accumulating MMA cuts its sum off at 24 bits
+// instead of rounding it, so O shrinks a little with every product: by 1e-7 of itself per
+// step (measured; 8 products each), 5e-5 over a run of 512 steps.  After this many steps O
+// is folded into a sum in the workspace, which rounds: 9e-6 of error however long the run.
+// (8 sequences of 8192 to 32768 tokens, 512 rows per kv head: 593 us without folds, 606 us
+// with one every 64 steps, 623 us every 32.)
+constexpr int TT_FOLD = 64;
 
 template <int D>
 struct TreeGeom {
@@ -177,6 +184,48 @@ __device__ __noinline__ bool tt_rescale(uint32_t o_col, uint32_t s_col, float al
         }
         tmem_store32_bits(col, pw);
     }
+    return true;
+}
+
+// Moves a row's O, which belongs to the running maximum m, into its sum in the workspace,
+// once `bar` says that none of the stream's P.V runs (fresh: the run's first fold), or,
+// back: adds that sum to O.  `at` keeps the sum's maximum.  Sum and maximum are
+// the thread's own.  Out of line like tt_rescale.
+template <int D>
+__device__ __noinline__ bool tt_fold(uint32_t o_col, float4* sum, int stride, float* at, float m, bool fresh, bool back, bool valid,
+                                     uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* dev_err) {
+    const bool done = tt_wait(bar, parity, abort_flag, dev_err);
+    if (!__all_sync(FULL_MASK, done)) return false;
+    tmem_fence_after_sync();
+    float e = 0.f;
+    if (valid && !fresh) {
+        const float before = *at;
+        e = before == NEG_INF ? 0.f : exp2_approx(before - m);
+    }
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = valid && !fresh ? __ldcg(sum + (c / 4 + k) * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float o[32];
+        tmem_load32(o_col + c, o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            o[4 * k + 0] = fmaf(v[k].x, e, o[4 * k + 0]);
+            o[4 * k + 1] = fmaf(v[k].y, e, o[4 * k + 1]);
+            o[4 * k + 2] = fmaf(v[k].z, e, o[4 * k + 2]);
+            o[4 * k + 3] = fmaf(v[k].w, e, o[4 * k + 3]);
+        }
+        if (back) {
+            tmem_store32(o_col + c, o);
+        } else if (valid) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                __stcg(sum + (c / 4 + k) * stride, make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+        }
+        __syncwarp();
+    }
+    if (valid && !back) *at = m;
     return true;
 }
 
@@ -416,7 +465,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                         const uint64_t vd = v_desc + ((v_slot * Geo::SLOT + half * (Geo::SLOT / 2)) >> 4);
                         const uint32_t p_tmem = utmem + TT_KT * w + TT_HT * buf;
                         const uint32_t o_tmem = utmem + Geo::O_COL + D * w;
-                        const uint32_t more = no >= 2 ? 1u : 0u;   // 0: the stream's first step of the run
+                        // 0: the stream's first step of the run, or the first since O was folded
+                        const uint32_t more = ((no >> 1) & (TT_FOLD - 1)) != 0 ? 1u : 0u;
 #pragma unroll
                         for (int kk = 0; kk < TT_HT / 16; ++kk) {
                             const uint32_t p = p_tmem + 32 * (kk / 2) + 8 * (kk % 2);
@@ -523,6 +573,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             float m = NEG_INF, l = 0.f;
             bool ok = __all_sync(FULL_MASK, !*abort_flag);
             const int steps = two ? 2 * nt : nt;
+            // O's folded sum: in the run's partial, where nothing lies yet (a run that leaves
+            // none uses the last one's), a row for every row of both streams
+            auto fold = [&](bool fresh, bool back) {
+                const int slot = 2 * blockIdx.x + (r.starts ? 0 : 1), i = two ? R : w * (a.part_rows / 2) + row;
+                return tt_fold<D>(o_col, reinterpret_cast<float4*>(tree_part(a, slot, D)) + i, a.part_rows,
+                                  &a.part_ml[static_cast<size_t>(slot) * a.part_rows + i].x, m, fresh, back, valid,
+                                  &sh.o_done[w][(use - 1) & 1u], ((use - 1) >> 1) & 1u, abort_flag, a.dev_err);
+            };
             for (int step = 0; step < steps && ok; ++step, ++use) {
                 const int j = two ? step >> 1 : step, h = two ? step & 1 : w;   // tile of the run, half of the tile
                 const uint32_t s_col = lanes + TT_KT * w + TT_HT * (use & 1u);
@@ -639,6 +697,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                     float s0, s1;
                     sum.get(s0, s1);
                     l += s0 + s1;
+                    if (step > 0 && step % TT_FOLD == 0) ok &= fold(step == TT_FOLD, false);
                 }
                 tmem_fence_before_sync();
                 mbar_arrive(smem_u32(&sh.p_full[w][use & 1u]));
@@ -646,6 +705,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             // the run's last P.V of this stream
             if (ok) ok = tt_wait(&sh.o_done[w][(use - 1) & 1u], ((use - 1) >> 1) & 1u, abort_flag, a.dev_err);
             tmem_fence_after_sync();
+            if (steps > TT_FOLD && busy && __all_sync(FULL_MASK, ok)) ok = fold(false, true);
 
             // epilogue.  Two row tiles: every stream stores its own rows.  One:
             // both streams hold a part of the same rows; each stores half of the
