@@ -10,6 +10,7 @@ has not been built.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -121,6 +122,12 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _allocating_for(stream: Optional[torch.cuda.Stream]):
+    """Context in which a call launched on ``stream`` allocates what it drops on return: memory of that
+    stream, which nobody else gets before the call's kernels are through with it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -197,7 +204,8 @@ def decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     dt = k_cache.dtype
     if workspace is None:
         cap = decode_capacity(block_tables, B, max_context_len)
-        workspace = alloc_workspace(S, Hq, d, cap, partition_size, q.device)
+        with _allocating_for(stream):
+            workspace = alloc_workspace(S, Hq, d, cap, partition_size, q.device)
     rc = lib.pa_decode_phases(
         _dev(out, "out"), dtype_code(out.dtype), _dev(q, "q", dt), _dev(k_cache, "k_cache", dt),
         _dev(v_cache, "v_cache", dt), _dev(block_tables, "block_tables", torch.int32),
@@ -233,7 +241,8 @@ def decode_step(out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, value: to
     dt = k_cache.dtype
     if workspace is None:
         cap = decode_capacity(block_tables, B, max_context_len)
-        workspace = alloc_workspace(S, Hq, d, cap, partition_size, q.device)
+        with _allocating_for(stream):
+            workspace = alloc_workspace(S, Hq, d, cap, partition_size, q.device)
     rc = lib.pa_decode_step(
         _dev(out, "out"), dtype_code(out.dtype), _dev(q, "q", dt), _dev(key, "key", dt) if T else None,
         _dev(value, "value", dt) if T else None, _dev(k_cache, "k_cache", dt), _dev(v_cache, "v_cache", dt),
@@ -265,7 +274,8 @@ def prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     if workspace is None:
         cap = decode_capacity(block_tables, B, max_context_len)
         n = lib.pa_prefill_workspace_bytes(T, Hq, d, cap, partition_size)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        with _allocating_for(stream):
+            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
     rc = lib.pa_prefill(
         _dev(out, "out"), dtype_code(out.dtype), _dev(q, "q", dt), _dev(k_cache, "k_cache", dt),
         _dev(v_cache, "v_cache", dt), _dev(block_tables, "block_tables", torch.int32),
@@ -355,7 +365,8 @@ def tree_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cac
         raise ValueError("mask must be [num_tokens][words]")
     dt = k_cache.dtype
     if workspace is None:
-        workspace = alloc_tree_workspace(T, Hq, d, q.device)
+        with _allocating_for(stream):
+            workspace = alloc_tree_workspace(T, Hq, d, q.device)
     rc = lib.pa_tree_decode(
         _dev(out, "out"), dtype_code(out.dtype), _dev(q, "q", dt), _dev(k_cache, "k_cache", dt),
         _dev(v_cache, "v_cache", dt), _dev(block_tables, "block_tables", torch.int32),
@@ -401,7 +412,8 @@ def decode_weights(out: torch.Tensor, weights_out: torch.Tensor, q: torch.Tensor
     dt = k_cache.dtype
     if workspace is None:
         cap = decode_capacity(block_tables, B, max_context_len)
-        workspace = alloc_weights_workspace(S, Hq, d, cap, partition_size, q.device)
+        with _allocating_for(stream):
+            workspace = alloc_weights_workspace(S, Hq, d, cap, partition_size, q.device)
     f32 = torch.float32
     rc = lib.pa_decode_weights(
         _dev(out, "out"), dtype_code(out.dtype), _dev(weights_out, "weights_out", f32),
