@@ -382,6 +382,8 @@ PA_API int pa_tree_mask(const int32_t* parents, int num_nodes, int mask_words, i
  * is a variant that serves every sequence by itself (shared blocks are read once
  * per sequence).  At most 256 query heads per kv head.  Totals are sums in fp32,
  * heads in order.  A token in a block whose id is flagged receives weight zero.
+ * A logit of NaN or +infinity makes the head's softmax NaN: its row of `out` (where
+ * pa_decode gives zeros) and the totals of its kv head, at every position of the context.
  * Calls that may overlap in time need workspaces of their own.
  */
 PA_API size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int head_dim,

@@ -489,6 +489,12 @@ __device__ __forceinline__ int unit_rows(const DecodeArgs& a, int hg, int count)
     return a.group <= 8 ? count * a.group : min(8, a.group - hg * 8);
 }
 
+// A row's output from its sums.  LOGITS (pa_decode_weights): a sum that is NaN, as a
+// logit of NaN or +infinity makes it, stays NaN; pa_decode gives zeros.
+__device__ __forceinline__ float normalised(float O, float L, bool logits) {
+    return L > 0.f || (logits && L != L) ? O / L : 0.f;
+}
+
 // row_info[n] = (sequence, head, partitions of that sequence) of query row n.
 // LOGITS: the (max, sum) of a single partition is kept too (pa_decode_weights).
 template <int W, int D, bool LOGITS>
@@ -500,10 +506,11 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, const float* 
 #pragma unroll
         for (int w = 0; w < W; ++w) M = fmaxf(M, mm[w * 8 + n]);
         float L = 0.f, O = 0.f;
-        if (M != NEG_INF) {
+        if (LOGITS || M != NEG_INF) {   // logits that are all NaN have no maximum, but a sum
+            const float base = M == NEG_INF ? 0.f : M;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                const float e = exp2_approx(mm[w * 8 + n] - M);
+                const float e = exp2_approx(mm[w * 8 + n] - base);
                 L += e * ml[w * 8 + n];
                 O += e * mo[(w * 8 + n) * D + d];
             }
@@ -511,7 +518,7 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, const float* 
         const int3 ri = row_info[n];
         const size_t row = static_cast<size_t>(ri.x) * a.num_heads + ri.y;
         if (ri.z <= 1) {
-            const float v = L > 0.f ? O / L : 0.f;
+            const float v = normalised(O, L, LOGITS);
             if (a.out_f32)
                 static_cast<float*>(a.out)[row * D + d] = v;
             else
@@ -1043,7 +1050,7 @@ attend_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if (ri.z <= 1) {
                 float v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = ml.y > 0.f ? O[k] / ml.y : 0.f;
+                for (int k = 0; k < 4; ++k) v[k] = normalised(O[k], ml.y, LOGITS);
                 if (a.out_f32)
                     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + d0) =
                         make_float4(v[0], v[1], v[2], v[3]);
@@ -1366,7 +1373,7 @@ __device__ __forceinline__ void reduce_head_warp(const DecodeArgs& a, int s, int
         const float r[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float val = L > 0.f ? r[k] / L : 0.f;
+            const float val = normalised(r[k], L, a.w_out != nullptr);
             if (a.out_f32)
                 static_cast<float*>(a.out)[row * D + 4 * c4 + k] = val;
             else
@@ -1435,7 +1442,8 @@ __global__ void __launch_bounds__(REDUCE_PARTS_THREADS, 4) reduce_parts_kernel(c
     const int c4 = tid % C4, g = tid / C4;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
-    if (M != NEG_INF) {
+    const float base = M == NEG_INF ? 0.f : M;
+    if (M != NEG_INF || a.w_out != nullptr) {
         for (int p0 = g; p0 < nparts; p0 += G * U) {
             float4 v[U];
             float2 ml[U];
@@ -1450,7 +1458,7 @@ __global__ void __launch_bounds__(REDUCE_PARTS_THREADS, 4) reduce_parts_kernel(c
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (p0 + u * G < nparts) {
-                    const float e = exp2_approx(ml[u].x - M);
+                    const float e = exp2_approx(ml[u].x - base);
                     L = fmaf(e, ml[u].y, L);
                     o.x = fmaf(e, v[u].x, o.x);
                     o.y = fmaf(e, v[u].y, o.y);
@@ -1470,7 +1478,7 @@ __global__ void __launch_bounds__(REDUCE_PARTS_THREADS, 4) reduce_parts_kernel(c
             O += reinterpret_cast<const float*>(&so[k][0])[d];
             Lt += sl[k];
         }
-        const float val = Lt > 0.f ? O / Lt : 0.f;
+        const float val = normalised(O, Lt, a.w_out != nullptr);
         if (a.out_f32)
             static_cast<float*>(a.out)[row * D + d] = val;
         else
@@ -1520,11 +1528,12 @@ __global__ void __launch_bounds__(WEIGHTS_THREADS) weights_kernel(const DecodeAr
         for (int p = lane; p < nparts; p += 32) M = fmaxf(M, ml[p].x);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL_MASK, M, off));
-        if (M != NEG_INF)
-            for (int p = lane; p < nparts; p += 32) L = fmaf(exp2_approx(ml[p].x - M), ml[p].y, L);
+        const float base = M == NEG_INF ? 0.f : M;
+        for (int p = lane; p < nparts; p += 32) L = fmaf(exp2_approx(ml[p].x - base), ml[p].y, L);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(FULL_MASK, L, off);
-        if (lane == 0) s_ml[n] = make_float2(M == NEG_INF ? 0.f : M, L > 0.f ? 1.f / L : 0.f);
+        // a sum that is NaN makes every weight of the head NaN; zero: no token takes part
+        if (lane == 0) s_ml[n] = make_float2(base, L != 0.f ? 1.f / L : 0.f);
     }
     __syncthreads();
     const int counted = a.w_lens != nullptr ? a.w_lens[s] : ctx;
