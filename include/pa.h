@@ -404,7 +404,8 @@ PA_API int pa_decode_weights(void* out, pa_dtype out_dtype, float* weights_out, 
  *
  *   keep          int32 [num_seqs][num_kv_heads][keep_stride]: the positions, ascending;
  *                 entries past keep_lens[s] are not written
- *   keep_lens     int32 [num_seqs]: min(context_lens[s], budgets[s]), the same for all heads
+ *   keep_lens     int32 [num_seqs]: min(context_lens[s], budgets[s]), the same for all heads;
+ *                 must not overlap context_lens or budgets (PA_ERR_INVALID_ARG)
  *   weights       fp32 [num_seqs][num_kv_heads][weights_stride] (pa_decode_weights)
  *   context_lens  int32 [num_seqs], clamped to [0, weights_stride] and flagged PA_DEVERR_CONTEXT
  *   budgets       int32 [num_seqs], clamped to [0, keep_stride] and flagged PA_DEVERR_CONTEXT

@@ -625,6 +625,12 @@ __global__ void __launch_bounds__(CMP_THREADS, 6) compact_kernel(const CompactAr
 
 using namespace pa;
 
+// Whether two arrays of n share an element.
+static bool overlap(const int32_t* a, const int32_t* b, int n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), bytes = sizeof(int32_t) * static_cast<size_t>(n);
+    return x < y + bytes && y < x + bytes;
+}
+
 extern "C" int pa_select_tokens(int32_t* keep, int32_t* keep_lens, const float* weights, const int32_t* context_lens,
                                 const int32_t* budgets, int num_seqs, int num_kv_heads, int weights_stride,
                                 int keep_stride, int recent, int32_t* dev_err, pa_stream stream) {
@@ -637,6 +643,8 @@ extern "C" int pa_select_tokens(int32_t* keep, int32_t* keep_lens, const float* 
         return PA_ERR_INVALID_ARG;
     const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
     if (rows * SEL_MAX_CLUSTER > INT_MAX) return PA_ERR_UNSUPPORTED;
+    // one CTA writes a sequence's keep_lens while those of its other heads still read the inputs
+    if (overlap(keep_lens, context_lens, num_seqs) || overlap(keep_lens, budgets, num_seqs)) return PA_ERR_INVALID_ARG;
     if (const int rc = device_check(weights)) return rc;
     SelectArgs a;
     a.keep = keep;
