@@ -73,7 +73,8 @@ typedef enum pa_status {
                                  num_heads not a multiple of num_kv_heads, ... */
     PA_ERR_UNSUPPORTED = 2,   /* head_dim not in {64, 128}, block_size not in {4, 8, 16, 32},
                                  partition_size not a positive multiple of 32 (or > 8192),
-                                 dtype combination not offered */
+                                 dtype combination not offered, more than 2^31 - 2^16 positions
+                                 in a row of the calls that drop tokens */
     PA_ERR_WORKSPACE = 3,     /* workspace_bytes below pa_decode_workspace_bytes() */
     PA_ERR_CUDA = 4,          /* a CUDA runtime call or a kernel launch failed */
     PA_ERR_DEVICE_INDEX = 5   /* the current CUDA device's index is beyond the library's

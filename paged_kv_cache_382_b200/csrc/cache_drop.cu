@@ -642,7 +642,8 @@ extern "C" int pa_select_tokens(int32_t* keep, int32_t* keep_lens, const float* 
         !aligned_to(budgets, 4))
         return PA_ERR_INVALID_ARG;
     const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
-    if (rows * SEL_MAX_CLUSTER > INT_MAX) return PA_ERR_UNSUPPORTED;
+    if (rows * SEL_MAX_CLUSTER > INT_MAX || weights_stride > MAX_POSITIONS || keep_stride > MAX_POSITIONS)
+        return PA_ERR_UNSUPPORTED;
     // one CTA writes a sequence's keep_lens while those of its other heads still read the inputs
     if (overlap(keep_lens, context_lens, num_seqs) || overlap(keep_lens, budgets, num_seqs)) return PA_ERR_INVALID_ARG;
     if (const int rc = device_check(weights)) return rc;
@@ -703,7 +704,8 @@ extern "C" int pa_compact(void* k_cache, void* v_cache, float* weights_out, cons
     if (keep_heads != 1 && keep_heads != num_kv_heads) return PA_ERR_INVALID_ARG;
     if (!(head_dim == 64 || head_dim == 128)) return PA_ERR_UNSUPPORTED;
     if (!(block_size == 4 || block_size == 8 || block_size == 16 || block_size == 32)) return PA_ERR_UNSUPPORTED;
-    if (static_cast<long long>(num_blocks) * num_kv_heads * block_size > INT_MAX) return PA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_blocks) * num_kv_heads * block_size > INT_MAX || keep_stride > MAX_POSITIONS)
+        return PA_ERR_UNSUPPORTED;
     if (static_cast<long long>(src_max_blocks) * block_size > INT_MAX ||
         static_cast<long long>(dst_max_blocks) * block_size > INT_MAX)
         return PA_ERR_INVALID_ARG;

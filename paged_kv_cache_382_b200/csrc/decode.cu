@@ -1769,7 +1769,7 @@ static int decode_impl(void* out, pa_dtype out_dtype, const void* q, const void*
     const int max_parts = parts_for(static_cast<int>(cap), partition_size);
     if (static_cast<long long>(num_seqs) * max_parts > (INT_MAX >> ITEM_LOW_BITS)) return PA_ERR_UNSUPPORTED;
     if (weights != nullptr) {
-        if (num_heads / num_kv_heads > WEIGHTS_MAX_GROUP ||
+        if (num_heads / num_kv_heads > WEIGHTS_MAX_GROUP || cap > MAX_POSITIONS ||
             static_cast<long long>(num_seqs) * num_kv_heads * (cap / WEIGHTS_TOKENS + 1) + static_cast<long long>(num_seqs) * num_heads > INT_MAX)
             return PA_ERR_UNSUPPORTED;
         if (!weights->out || !aligned_to(weights->out, 4) || (weights->in && !aligned_to(weights->in, 4)) ||

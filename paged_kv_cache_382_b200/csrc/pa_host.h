@@ -7,6 +7,7 @@
 #include <stdio.h>
 
 #include <atomic>
+#include <climits>
 #include <mutex>
 #include <utility>
 
@@ -25,6 +26,10 @@ inline int element_bytes(pa_dtype dt) { return dt == PA_BF16 ? 2 : 4; }
 inline bool valid_dtype(int dt) { return dt == PA_F32 || dt == PA_BF16; }
 
 constexpr int MAX_DEVICES = 64;
+
+// Positions of a row that is worked through in tiles, segments or pages: their ends, past the
+// row's own, still fit 32 bits.
+constexpr int MAX_POSITIONS = INT_MAX - (1 << 16);
 
 // Checks, right before a launch, that the current device can be served and that
 // `buf` (a buffer the launch reads or writes; may be null) lives on it:

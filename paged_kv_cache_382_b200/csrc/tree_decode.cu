@@ -412,6 +412,7 @@ extern "C" int pa_tree_decode(void* out, pa_dtype out_dtype, const void* q, cons
     if (static_cast<long long>(max_blocks_per_seq) * block_size > INT_MAX) return PA_ERR_INVALID_ARG;
     long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
     if (max_context_len > 0 && max_context_len < cap) cap = max_context_len;
+    if (cap > MAX_POSITIONS) return PA_ERR_UNSUPPORTED;
     // the work line is counted in 32 bits: at most this many half row blocks, each
     // with a step per 64-token tile
     const long long halves = static_cast<long long>(num_tokens) * num_heads / TS_ROWS +

@@ -19,3 +19,25 @@ def pa():
 def test_select_refuses_lengths_over_its_inputs(pa, lens, ctx, budgets, S):
     """keep_lens is written by one CTA of a sequence while others read the lengths and budgets."""
     assert pa.lib.pa_select_tokens(8 * P, lens, 4 * P, ctx, budgets, S, 2, 64, 64, 3, None, None) == pa.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("stride,width", [(2 ** 31 - 1, 64), (2 ** 31 - 2 ** 15, 64), (64, 2 ** 31 - 1)])
+def test_rows_near_the_end_of_32_bits(pa, stride, width):
+    """A kernel's segments and pages end past the row's own end, which still has to fit 32 bits."""
+    assert pa.lib.pa_select_tokens(8 * P, P, 4 * P, 2 * P, 3 * P, 2, 2, stride, width, 3, None, None) == pa.PA_ERR_UNSUPPORTED
+    if width > 64:
+        assert pa.lib.pa_compact(P, P, None, None, 0, P, P, 4, 4, P, 2, width, None, P, 1, 2, 64, 16, 8, 1, None,
+                                 None) == pa.PA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("blocks,bound,ok", [(2 ** 27 - 1, 0, False), (2 ** 27 - 1, 2 ** 31 - 100, False), (2 ** 27 - 1, 4096, True)])
+def test_tree_contexts_near_the_end_of_32_bits(pa, blocks, bound, ok):
+    rc = pa.lib.pa_tree_decode(P, 0, P, P, P, P, P, P, P, 1, 1, 0 if ok else 6, 4, 2, 64, 16, 8, blocks, bound, 0.1, P, 1 << 30, 1, None,
+                               None)
+    assert rc == (pa.PA_OK if ok else pa.PA_ERR_UNSUPPORTED)
+
+
+def test_weights_of_contexts_near_the_end_of_32_bits(pa):
+    n = 2 ** 27 - 1
+    assert pa.lib.pa_decode_weights(P, 0, P, None, None, 2 ** 31 - 1, P, P, P, P, P, 1, 4, 2, 64, 16, 8, n, 0, 0.1, 8192, P, 1 << 40, 0,
+                                    None, None) == pa.PA_ERR_UNSUPPORTED
