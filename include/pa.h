@@ -310,7 +310,8 @@ PA_API int pa_decode_noalloc(void* out, pa_dtype out_dtype, const void* q, const
  * pa_tree_decode -- attention of drafted tokens against the paged context: the
  * verification step of speculative decoding.  The drafted tokens ("nodes") of a
  * sequence form a tree; all of them are in the pool already, behind the prefix
- * (write them with pa_reshape_and_cache first), and all are verified at once.
+ * (write them with pa_reshape_and_cache first; pa_bm_append with prefix caching wants
+ * ids below zero for them), and all are verified at once.
  * Node i of sequence s (of n_s = query_start[s+1] - query_start[s]) sits at position
  * context_lens[s] - n_s + i and attends to every position below
  * context_lens[s] - n_s and to the nodes its mask row names (its ancestors and
@@ -489,7 +490,10 @@ PA_API int pa_bm_free(pa_block_manager* manager, int64_t seq_id);
  * cache); copies[2 * max_copies] receives the (src, dst) block copies that must
  * run before the writes (may be NULL if max_copies is 0), *num_copies their
  * number, *num_cached_tokens (nullable) the tokens served from the cache.
- * token_ids[num_tokens] is required with prefix caching, else ignored.
+ * token_ids[num_tokens] is required with prefix caching, else ignored.  Give the nodes
+ * of a drafted tree an id below zero: their K and V do not follow from the ids before
+ * them, so their blocks and those behind them are neither cached nor looked up until
+ * pa_bm_compact has cut the sequence back to where they began.
  * PA_ERR_WORKSPACE if the pool runs out of free blocks or more than max_copies
  * copies are needed: the tokens before that point stay appended.
  */

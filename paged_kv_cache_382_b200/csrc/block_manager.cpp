@@ -39,6 +39,7 @@ struct Sequence {
     std::vector<uint64_t> hashes;         // chained hash of every full block
     std::vector<int32_t> tokens;          // every token's id
     bool keyed = true;                    // ids known: false from an eviction on (blocks no longer cached)
+    int64_t first_draft = INT64_MAX;      // position of the first token with an id below zero
 };
 
 }  // namespace
@@ -172,16 +173,18 @@ extern "C" int pa_bm_free(pa_block_manager* m, int64_t seq_id) {
 namespace {
 
 // Prefix caching: token `id` now stands at the end of sq's block b; a block it
-// fills is cached.
+// fills is cached.  K and V of a drafted token (an id below zero) do not follow from
+// the ids before it: its block and those behind it are not.
 void note_token(pa_block_manager* m, Sequence& sq, int32_t b, int32_t id) {
     const int B = m->block_size;
+    if (id < 0 && sq.first_draft == INT64_MAX) sq.first_draft = static_cast<int64_t>(sq.tokens.size());
     sq.tokens.push_back(id);
     sq.partial_tokens.push_back(id);
     if (static_cast<int>(sq.partial_tokens.size()) < B) return;
     const uint64_t h = chain_hash(sq.last_full_hash, sq.partial_tokens.data(), B);
     sq.last_full_hash = h;
     sq.hashes.push_back(h);
-    if (m->block_hash[b] == 0 && !m->cached.count(h)) {
+    if (sq.first_draft == INT64_MAX && m->block_hash[b] == 0 && !m->cached.count(h)) {
         m->cached.emplace(h, b);
         m->block_hash[b] = h;
         std::copy(sq.partial_tokens.begin(), sq.partial_tokens.end(),
@@ -203,7 +206,7 @@ int append_tokens(pa_block_manager* m, Sequence& sq, const int32_t* token_ids, i
         const int off = static_cast<int>(pos % B);
         if (off == 0 && logical == static_cast<int64_t>(sq.table.size())) {
             // a new logical block: reuse a cached one if the next B tokens form a known block
-            if (m->prefix_cache && sq.keyed && num_tokens - i >= B) {
+            if (m->prefix_cache && sq.keyed && sq.first_draft == INT64_MAX && num_tokens - i >= B) {
                 const uint64_t h = chain_hash(sq.last_full_hash, token_ids + i, B);
                 auto hit = m->cached.find(h);
                 if (hit != m->cached.end()) {
@@ -313,6 +316,7 @@ void rekey(pa_block_manager* m, Sequence& sq, int64_t unchanged, int64_t num_tok
     sq.tokens.resize(static_cast<size_t>(unchanged));
     sq.last_full_hash = sq.hashes.empty() ? 0 : sq.hashes.back();
     sq.partial_tokens.assign(sq.tokens.begin() + static_cast<std::ptrdiff_t>(unchanged / B * B), sq.tokens.end());
+    if (unchanged <= sq.first_draft) sq.first_draft = INT64_MAX;
     for (int64_t p = unchanged; p < num_tokens; ++p)
         note_token(m, sq, sq.table[static_cast<size_t>(p / B)], ids[p - unchanged]);
 }

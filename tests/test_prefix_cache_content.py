@@ -60,6 +60,17 @@ class Cache:
         self.known[s].append(int(token))
         return self.chain(self.known[s])
 
+    def draft(self, s, tokens):
+        """A tree of drafted tokens: values of their own, for no ids say what a node's ancestors are."""
+        slots, copies, cached = self.bm.append(s, [-1] * len(tokens))
+        assert cached == 0
+        self.copy(copies)
+        for at, _ in zip(slots, tokens):
+            self.unique -= 1
+            self.seqs[s].append(self.unique)
+            self.slots[at] = self.unique
+        self.check()
+
     def append(self, s, tokens):
         slots, copies, cached = self.bm.append(s, tokens)
         self.copy(copies)
@@ -158,3 +169,47 @@ def test_random_appends_forks_cuts_evictions_and_frees(pa, seed):
             if c.bm.num_free > sum(-(-(x + len(k)) // B) for x, k in zip(u, keeps)):
                 c.compact(some, u, keeps)
     assert nxt > 20
+
+
+def test_drafted_trees_do_not_enter_the_cache(pa):
+    """Two requests draft trees of several blocks behind the same prefix; neither finds the other's nodes, nor does a
+    request whose prompt runs on with the drafted tokens, during the verification or after it."""
+    c = Cache(pa, 64, 4)
+    for s in (1, 2):
+        c.add(s)
+        assert c.append(s, range(1, 11)) == (0 if s == 1 else 8)
+        c.draft(s, range(20, 33))
+    c.add(3)
+    assert c.append(3, list(range(1, 11)) + list(range(20, 33))) == 8
+    # the accepted path, by its ids: its values are those of the chain
+    names, paths = [1, 2], [[20, 22, 25], [21]]
+    accepted = {s: [10 + t - 20 for t in p] for s, p in zip(names, paths)}
+    for s, p in zip(names, paths):
+        for k, at in enumerate(accepted[s]):
+            v = c.chain(list(range(1, 11)) + p[: k + 1])
+            table = c.bm.block_table(s)
+            c.seqs[s][at] = v
+            c.slots[table[at // 4] * 4 + at % 4] = v
+    c.compact(names, [10, 10], [accepted[s] for s in names], ids=paths)
+    c.append(1, [40, 41, 42])
+    c.append(2, [40])
+    c.add(4)
+    assert c.append(4, list(range(1, 11)) + [20, 22, 25, 40, 41, 42]) == 16
+    c.add(5)
+    assert c.append(5, list(range(1, 11)) + [21, 40]) == 12
+    c.draft(5, range(9))
+    c.compact([5], [12], [[]])               # nothing accepted
+    c.append(5, [50, 51, 52, 53])
+    c.add(6)
+    assert c.append(6, list(range(1, 11)) + [21, 40, 50, 51, 52, 53]) == 16
+
+
+def test_blocks_behind_a_draft_are_not_cached(pa):
+    c = Cache(pa, 64, 4)
+    for s in (1, 2):
+        c.add(s)
+        c.append(s, [1, 2, 3])
+        c.draft(s, [7])
+        c.known[s] = None                    # what follows depends on the node
+        assert c.append(s, [5, 6, 7, 8]) == 0
+    assert not set(c.bm.block_table(1)) & set(c.bm.block_table(2))
