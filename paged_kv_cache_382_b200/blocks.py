@@ -137,6 +137,8 @@ class BlockManager:
         past a new length is dropped.  Returns the (src, dst) block copies that must run before the
         moves (for blocks that also hold unchanged tokens)."""
         B = self.block_size
+        if not len(seqs) == len(unchanged) == len(num_tokens) or len({id(seq) for seq in seqs}) != len(seqs):
+            raise ValueError("one length each for sequences that are named once")
         for seq, u, n in zip(seqs, unchanged, num_tokens):
             if not 0 <= u <= n <= seq.num_tokens:
                 raise ValueError("0 <= unchanged <= num_tokens <= the sequence's tokens")

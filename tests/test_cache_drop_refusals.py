@@ -41,3 +41,20 @@ def test_weights_of_contexts_near_the_end_of_32_bits(pa):
     n = 2 ** 27 - 1
     assert pa.lib.pa_decode_weights(P, 0, P, None, None, 2 ** 31 - 1, P, P, P, P, P, 1, 4, 2, 64, 16, 8, n, 0, 0.1, 8192, P, 1 << 40, 0,
                                     None, None) == pa.PA_ERR_UNSUPPORTED
+
+
+def test_python_manager_refuses_what_the_native_one_does():
+    """A sequence named twice, lengths that are not one per sequence or do not fit it: nothing changes."""
+    from paged_kv_cache_382_b200.blocks import BlockManager, BlockPool
+
+    pool = BlockPool(8)
+    bm = BlockManager(pool, 4)
+    a = bm.new_sequence()
+    bm.append_tokens(a, 10)
+    b = bm.fork(a)
+    before = (list(a.block_table), list(b.block_table), a.num_tokens, pool.num_free, pool.ref_cnt.tolist())
+    for seqs, u, n in [([a, a], [0, 0], [4, 4]), ([a, b], [0], [4]), ([a], [0], [4, 4]), ([a, b], [0, 5], [4, 4]), ([a, b], [0, 0], [4, 11])]:
+        with pytest.raises(ValueError):
+            bm.compact(seqs, u, n)
+        assert before == (list(a.block_table), list(b.block_table), a.num_tokens, pool.num_free, pool.ref_cnt.tolist())
+    assert bm.compact([a, b], [4, 0], [4, 4]) == []
