@@ -331,7 +331,8 @@ PA_API int pa_decode_noalloc(void* out, pa_dtype out_dtype, const void* q, const
  *   workspace     pa_tree_workspace_bytes(num_tokens, num_heads, head_dim) bytes, 256-byte
  *                 aligned, whatever the contexts; its contents need no initialisation
  * A row that sees nothing is zero.  More nodes than context: PA_DEVERR_CONTEXT, positions
- * below zero do not exist.  Other arguments and errors as for pa_decode.
+ * below zero do not exist.  Other arguments and errors as for pa_decode.  Every sequence
+ * is served by itself: blocks that several share are read once for each.
  * Arithmetic: as for pa_decode.  The work is cut over the GPU by the whole batch, so the same
  * call gives the same bits every time, but a sequence's rounding may differ in another batch.
  * On bf16 pools (pa_tree_uses_tensor_cores) the products run as

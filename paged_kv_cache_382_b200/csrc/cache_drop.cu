@@ -38,7 +38,8 @@ namespace pa {
 // when most totals are equal, the cluster makes the other passes too.  A segment's
 // keys are read once, all loads at the same time, and stay with their threads, in
 // registers or, 32 to a thread, in shared memory (up to 131072 candidates to a row;
-// longer rows are read again, from L2).
+// longer rows are read again, from L2: that takes 74 us instead of 56 on 64 rows of
+// 131072; 64 rows of 200000 take 114 us, 8 of them 41 us).
 // ---------------------------------------------------------------------------
 
 constexpr int SEL_THREADS = 512;
@@ -370,10 +371,13 @@ __global__ void __launch_bounds__(SEL_THREADS, 2) select_kernel(const SelectArgs
 // A thread finds the pool rows of one (source, destination) pair of a page of
 // THREADS pairs, its position and table entries fetched one and two pages ahead;
 // the threads that move a row's columns read the pair from shared memory.  Every
-// column's thread finding the rows itself took 1.2 times as long.
+// column's thread finding the rows itself took 1.6 times as long (64 sequences of 128
+// to 2048 tokens cut to a half, 32 kv heads: 306 against 194 us).
 // With many walks that is bound by HBM.  With few (a CTA per SM or less) the round
 // trips of a chunk would bound it: compact_few_kernel's CTAs have 1024 threads,
-// find 8192 pairs at once and keep four chunks of rows in flight.
+// find 8192 pairs at once and keep four chunks of rows in flight.  One sequence of 8
+// kv heads, d 128, bf16, to a quarter: 32768 tokens 20 against 43 us, 4096 tokens 5.3
+// against 6.4 us (in place 20 against 39).
 // ---------------------------------------------------------------------------
 
 constexpr int CMP_THREADS = 256, CMP_FEW_THREADS = 1024;
@@ -660,8 +664,10 @@ extern "C" int pa_select_tokens(int32_t* keep, int32_t* keep_lens, const float* 
     a.recent = recent;
     const int sms = current_sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
-    // As few CTAs to a row as hold its keys in registers, then more while that leaves
-    // SMs idle: a cluster's barriers cost more than longer segments do.
+    // As few CTAs to a row as hold its keys, then more while that leaves SMs idle: a
+    // cluster's barriers cost more than longer segments do (2048 rows of 4097: 85 us with
+    // one CTA, 147 with two; 64 rows of 32768: 17 us with two or four, 25 with eight; 8
+    // rows of 4097: 9.3 us with one, 8.7 with two).
     int cluster = 1;
     auto segment = [&](int c) { return ((weights_stride + c - 1) / c + 31) & ~31; };
     while (cluster < SEL_MAX_CLUSTER && segment(cluster) > sel_keys(SEL_Q_LONG)) cluster *= 2;
@@ -723,7 +729,9 @@ extern "C" int pa_compact(void* k_cache, void* v_cache, float* weights_out, cons
     const int sms = current_sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
     // Whole rows per CTA while (sequences x heads x pools) fill the GPU; below
-    // that rows are cut into slices of at least 32 bytes (a memory sector).
+    // that rows are cut into slices of at least 32 bytes (a memory sector).  One
+    // sequence of 8 kv heads, 32768 tokens to 8192: 20 us with 32-byte slices, 40 with 128,
+    // 70 with whole rows of 256; 8 sequences of 4096 to 1024: 20, 18 and 25 us.
     int log2_vecs = 0;
     while ((1 << log2_vecs) < row_vecs) ++log2_vecs;
     const long long pairs = 2LL * num_seqs * num_kv_heads;

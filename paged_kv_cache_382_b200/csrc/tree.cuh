@@ -242,7 +242,7 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, in
 }
 
 // Attend on the tensor cores (tree_tc.cu): bf16 pools, head_dim 64 or 128,
-// blocks of 8, 16 or 32 tokens, any group.
+// blocks of 4, 8, 16 or 32 tokens, any group.
 bool tree_tc_eligible(pa_dtype dtype, int block_size);
 int tree_tc_rows();
 int launch_tree_tc(const TreeArgs& a, int head_dim, int ctas, cudaStream_t st);

@@ -1,7 +1,7 @@
 // tree_decode.cu -- pa_tree_decode: attention of a tree of drafted tokens over
 // a paged cache.  The entry point, the attend kernel on the CUDA cores (fp32
-// pools), the join of cut units, and the host-side construction of masks from parents (pa_tree_mask).  tree.cuh says
-// what is computed and how the work is cut.
+// pools), the join of cut units, and the host-side construction of masks from
+// parents (pa_tree_mask).  tree.cuh says what is computed and how the work is cut.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
