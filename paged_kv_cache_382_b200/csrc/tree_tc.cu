@@ -151,7 +151,7 @@ __device__ __forceinline__ bool tt_wait(uint64_t* bar, uint32_t parity, volatile
 
 // A row's maximum was raised before chunk c of a step: scales what was summed with
 // the old one, O (when scale_o, once `bar` says that none of the stream's P.V runs)
-// and the step's weights before chunk c.  Out of
+// and the step's weights before chunk c, which are rounded to their 16 bits again.  Out of
 // line: it is rare, and the loop that calls it has to stay small for the
 // instruction caches (inlined, the softmax took 1.3 times as long).
 template <int D>
