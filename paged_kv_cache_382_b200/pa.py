@@ -543,8 +543,9 @@ class NativeBlockManager:
         _check(lib.pa_bm_free(self._h, seq_id), "pa_bm_free")
 
     def append(self, seq_id: int, tokens):
-        """Append tokens (a count, or token ids when prefix caching).  Returns
-        (slots int64 array, [(src, dst) copies], tokens served from the cache)."""
+        """Append tokens (a count, or token ids when prefix caching; ids below zero for the nodes of
+        a drafted tree, whose blocks the cache leaves out).  Returns (slots int64 array,
+        [(src, dst) copies], tokens served from the cache)."""
         np = self._np
         ids = None
         if isinstance(tokens, int):
